@@ -121,7 +121,8 @@ KDV_API const char* kdv_status_string(kdv_status s);
  * KDV_DERR_RANGE, and retires KDV_IMPL_TC_1SM; 121 adds kdv_absorb_q_ex /
  * kdv_unabsorb_o_ex; 122 adds kdv_verify_attn_launches; 123: KDV_IMPL_TC_STAGED
  * stages k_rope and q_lat in fp16 instead of whole bf16 rows (another
- * workspace size). */
+ * workspace size); the kdv_rope*, kdv_latent8_write, kdv_verify_attn8* and
+ * kdv_logits_process entry points joined 123 without changing what it had. */
 KDV_API int32_t kdv_version(void);
 
 /*
@@ -435,6 +436,231 @@ typedef struct kdv_tree_build_params {
   int32_t* d_err;             /* nullable device error flag                          */
 } kdv_tree_build_params;
 KDV_API kdv_status kdv_tree_build(const kdv_tree_build_params* p, void* stream);
+
+/*
+ * Rotary positions (this library's operator; the pages assume rotated inputs).
+ * For head vector x of token i at position pos_i, pair k (0 <= k < rot_dim/2)
+ * is turned by the angle pos_i * inv_freq[k] and scaled by mscale:
+ *   (u, v) -> mscale * (u cos a - v sin a, u sin a + v cos a).
+ * KDV_ROPE_INTERLEAVED pairs elements (2k, 2k+1), KDV_ROPE_HALF (k, k +
+ * rot_dim/2). Elements rot_dim..dim-1 are copied. inverse = 1 turns by -a:
+ * the transpose, so it is the gradient of the forward turn (mscale included)
+ * and moves already rotated rows back. Angles are formed in 64 bits, so
+ * positions up to 2^31 keep an fp32 result's accuracy.
+ */
+#define KDV_ROPE_INTERLEAVED 0
+#define KDV_ROPE_HALF 1
+#define KDV_MAX_ROT 256 /* largest rot_dim */
+
+/* Rules of kdv_rope_freqs (base^(-2k/rot_dim) unscaled). */
+#define KDV_ROPE_SCALE_NONE 0
+#define KDV_ROPE_SCALE_LINEAR 1 /* every frequency divided by factor */
+#define KDV_ROPE_SCALE_NTK 2    /* base * factor^(rot_dim / (rot_dim - 2)) */
+#define KDV_ROPE_SCALE_YARN 3   /* divided by factor below beta_slow turns over
+                                   trained_len, kept above beta_fast, a linear
+                                   ramp over the pair index between */
+
+/*
+ * kdv_rope_freqs -- the rot_dim/2 inverse frequencies, in 64 bits, into HOST
+ * memory inv_freq, and (nullable) the magnitude factor: 0.1 ln(factor) + 1
+ * for YARN, 1 otherwise. HOST only, no device work. rot_dim even in
+ * [2, KDV_MAX_ROT] (NTK: > 2), base > 1, factor >= 1; YARN: trained_len >= 1
+ * and beta_fast > beta_slow > 0 (else KDV_ERR_INVALID_ARG; the arguments a
+ * rule does not use are ignored).
+ */
+KDV_API kdv_status kdv_rope_freqs(int32_t rot_dim, double base, int32_t rule, double factor, double trained_len,
+                                  double beta_fast, double beta_slow, double* inv_freq, double* mscale);
+
+typedef struct kdv_rope_params {
+  int32_t tokens;          /* n >= 0 (0: nothing is launched)                    */
+  int32_t heads;           /* >= 1                                               */
+  int32_t dim;             /* >= 1 elements of a head vector                     */
+  int32_t rot_dim;         /* even, in [2, min(dim, KDV_MAX_ROT)]                */
+  int32_t layout;          /* KDV_ROPE_INTERLEAVED / KDV_ROPE_HALF               */
+  int32_t inverse;         /* 0 / 1                                              */
+  int32_t x_dtype;         /* KDV_BF16 / KDV_F32                                 */
+  int32_t y_dtype;
+  const void* x;           /* element (i, h, d) at i*x_token_stride + h*x_head_stride + d */
+  int64_t x_token_stride;
+  int64_t x_head_stride;   /* |stride| >= dim when heads > 1                     */
+  void* y;                 /* out; may be x itself with its strides and type, no other overlap */
+  int64_t y_token_stride;
+  int64_t y_head_stride;
+  const int32_t* pos;      /* [n] positions (any int32), or NULL: token i is tree node i and
+                              pos = prefix_len[b] + depth[i] of its request b    */
+  int32_t batch;           /* with pos NULL: B in [1, KDV_MAX_BATCH]             */
+  const int32_t* tree_off; /* [B+1] device CSR over the n nodes                  */
+  const int32_t* prefix_len;   /* [B] device                                     */
+  const int32_t* depth;    /* [n] device, from kdv_tree_mask_build               */
+  const double* h_inv_freq;    /* HOST [rot_dim/2], read during the call         */
+  float mscale;            /* finite (1 = a pure rotation)                       */
+} kdv_rope_params;
+
+/* kdv_rope -- y = mscale R(pos) x. Rows 16-byte aligned in base and strides
+ * (and rot_dim a multiple of 8, 16 for KDV_ROPE_HALF, dim of 8) take 16-byte
+ * accesses; any other layout takes a scalar path with the same results. */
+KDV_API kdv_status kdv_rope(const kdv_rope_params* p, void* stream);
+
+/*
+ * The 8-bit latent cache. Pool slot r holds scale x (c8[r] || kr[r]) with
+ *   c8 [num_slots][D_c]  e4m3 codes of the latent part (448 the largest, no infinity),
+ *   kr [num_slots][D_r]  bf16, the rotated rope part, divided by the same scale,
+ *   kv_scale [ceil(num_slots / scale_block)] fp32, one scale for every block of
+ *   scale_block consecutive slots (a power of two in [1, 4096]).
+ * 644 bytes a token at D_c = 512, D_r = 64, scale_block = 1, against 1152 in bf16.
+ *
+ * kdv_latent8_write -- quantises rows into the cache: kr is rotated first
+ * when h_inv_freq is given. Row i goes to slot[i] (-1: the row is skipped), or,
+ * with slot NULL, row i is tree node i: u = i - tree_off[b] of its request b
+ * goes to logical key prefix_len[b] + u, addressed as in kdv_verify_attn.
+ *   static_scale = 0 (needs scale_block 1): the row's scale is the least power
+ *     of two, at least 2^-100, with amax |c| <= 448 scale (1 for a row of
+ *     zeros), and is written to kv_scale. Dividing by it is exact.
+ *   static_scale = 1: kv_scale is read; values beyond 448 scale saturate. A
+ *     scale that is not finite and positive: KDV_DERR_RANGE, row not written.
+ * c8 = e4m3(c / scale), kr = bf16(R k / scale), each rounded once to nearest
+ * even. A c value that is NaN or infinite is stored as the e4m3 NaN and reported
+ * (KDV_DERR_RANGE; it is left out of amax). KDV_DERR_BAD_SLOT: slot outside
+ * [0, num_slots), row not written. KDV_DERR_BAD_LENGTH: a node beyond its
+ * request's kv_off range or outside tree_off. Two rows of one call given the
+ * same slot leave that slot unspecified (some mix of the two), others are right.
+ */
+typedef struct kdv_latent8_params {
+  int32_t rows;            /* n >= 0                                             */
+  int32_t d_latent;        /* D_c in [1, 512]                                    */
+  int32_t d_rope;          /* D_r in [0, 64]                                     */
+  int32_t dtype;           /* KDV_BF16 / KDV_F32: c and k_rope                   */
+  const void* c;           /* [n][c_stride] latent rows                          */
+  int64_t c_stride;        /* >= D_c                                             */
+  const void* k_rope;      /* [n][k_stride] rope rows (unused when D_r = 0)      */
+  int64_t k_stride;        /* >= D_r                                             */
+  const int32_t* slot;     /* [n] device, or NULL (tree nodes)                   */
+  int32_t batch;           /* tree nodes: B in [1, KDV_MAX_BATCH]                */
+  const int32_t* tree_off;     /* [B+1] device: tree nodes, or positions without pos */
+  const int32_t* prefix_len;   /* [B] device, likewise                           */
+  const int32_t* depth;        /* [n] device: positions without pos              */
+  const int32_t* kv_off;       /* [B+1] device: tree nodes                       */
+  const int32_t* page_table;   /* nullable: tree nodes                           */
+  const double* h_inv_freq;    /* HOST [rot_dim/2], or NULL: k_rope is stored as it is */
+  int32_t rot_dim;             /* with h_inv_freq: even, in [2, D_r]             */
+  int32_t layout;
+  float mscale;
+  const int32_t* pos;          /* [n] positions, or NULL: prefix_len + depth     */
+  uint8_t* c8;
+  void* kr;                    /* unused when D_r = 0                            */
+  float* kv_scale;
+  int64_t num_slots;
+  int32_t scale_block;
+  int32_t static_scale;
+  int32_t* d_err;              /* nullable device error flag                     */
+} kdv_latent8_params;
+KDV_API kdv_status kdv_latent8_write(const kdv_latent8_params* p, void* stream);
+
+/*
+ * kdv_verify_attn8 -- kdv_verify_attn over the 8-bit latent cache:
+ *   s[t,h,j] = scale * kv_scale_j * (q_lat[t,h] . c8[j] + q_rope[t,h] . kr[j])
+ *   o_lat[t,h] = sum_j softmax_j(s) kv_scale_j c8[j],  lse as kdv_verify_attn.
+ * Trees, masks, page tables and key addressing are those of kdv_verify_attn.
+ * mask NULL is a chain: node t sees the prefix and nodes 0..t of its request
+ * (one token: T = 1). A node whose mask is 0 sees the prefix alone; a row that
+ * sees no key gives o = 0 and lse = -inf. Keys that a row does not see never
+ * reach its outputs, whatever their rows hold (NaN codes and scales among it);
+ * a key it sees whose row holds a NaN gives NaN. A key whose slot is outside the
+ * pool is left out (KDV_DERR_BAD_SLOT); a request whose kv_off range is shorter
+ * than L + T has no keys (KDV_DERR_BAD_LENGTH).
+ * The tensor-core kernel (KDV_IMPL_TC, AUTO's choice where it applies) takes
+ * bf16 q, D_c = 512, D_r = 64, scale > 0, 16-byte aligned q, c8, kr, o and q rows;
+ * KDV_IMPL_SIMT takes any D_c <= 512, D_r <= 64 and fp32 q.
+ */
+typedef struct kdv_verify8_params {
+  int32_t batch;           /* B in [1, KDV_MAX_BATCH]                            */
+  int32_t num_heads;
+  int32_t d_latent;
+  int32_t d_rope;
+  float scale;
+  int32_t dtype;           /* KDV_BF16 / KDV_F32: q                              */
+  int32_t out_dtype;       /* KDV_BF16 / KDV_F32: o                              */
+  int32_t impl;            /* KDV_IMPL_AUTO / _SIMT / _TC                        */
+  const void* q;           /* [sumT*H][q_row_stride], row = q_lat || q_rope      */
+  int64_t q_row_stride;    /* 0 means D_c + D_r                                  */
+  const uint8_t* c8;       /* the cache, as above                                */
+  const void* kr;
+  const float* kv_scale;
+  int32_t scale_block;
+  int64_t num_slots;
+  const int32_t* page_table;   /* nullable                                       */
+  const int32_t* kv_off;       /* [B+1] device                                   */
+  const int32_t* tree_off;     /* [B+1] device                                   */
+  const int32_t* prefix_len;   /* [B] device, nullable: checked against host     */
+  const int32_t* h_prefix_len; /* [B] HOST                                       */
+  const int32_t* h_tree_T;     /* [B] HOST, each in [1, 64]                      */
+  const uint64_t* mask;        /* [sumT], or NULL (chain)                        */
+  int32_t num_splits;          /* 0 = auto, else S for every request             */
+  void* o;                     /* [sumT*H][D_c] out                              */
+  float* lse;                  /* [sumT*H] out, nullable                         */
+  void* workspace;             /* >= kdv_verify_attn8_workspace, 16-byte aligned; a call
+                                  in flight owns it                              */
+  size_t workspace_bytes;
+  int32_t* d_err;              /* nullable device error flag                     */
+  uint64_t wait_limit_ns;      /* as in kdv_verify_params                        */
+} kdv_verify8_params;
+KDV_API kdv_status kdv_verify_attn8_workspace(const kdv_verify8_params* p, size_t* bytes);
+/* Splits per request (nullable) and work items (nullable) of the call. */
+KDV_API kdv_status kdv_verify_attn8_plan(const kdv_verify8_params* p, int32_t* splits, int32_t* grid_items);
+KDV_API kdv_status kdv_verify_attn8(const kdv_verify8_params* p, void* stream);
+
+/*
+ * kdv_logits_process -- what a sampler does to the target logits of a tree
+ * before kdv_tree_accept. For node t of request b and token v:
+ *   made  = times v occurs in hist[b][prompt_len[b] .. hist_len[b]) plus on
+ *           node t's path (itself included; roots are left out: a root holds
+ *           the last committed token, which the history has already)
+ *   seen  = made > 0 or v in hist[b][0 .. prompt_len[b])
+ *   x = logits[t][v];  if seen: x > 0 ? x / repetition : x * repetition
+ *   x = x - frequency * made - presence * [made > 0] + bias_b[v]
+ *   out = -inf where the node's allow row has bit v clear, else x.
+ * Arithmetic in fp32, rounded once to out_dtype. NaN logits stay NaN unless
+ * their bit is clear.
+ */
+typedef struct kdv_logits_params {
+  int32_t batch;           /* B in [1, KDV_MAX_BATCH]                            */
+  int32_t max_T;           /* [1, 64]: bound on every T_b                        */
+  int32_t total_nodes;     /* sumT (HOST value; rows of logits and out)          */
+  int32_t vocab;           /* V >= 1                                             */
+  int32_t dtype;           /* KDV_BF16 / KDV_F32                                 */
+  int32_t out_dtype;
+  const void* logits;      /* [sumT][logits_ld]                                  */
+  int64_t logits_ld;       /* >= V                                               */
+  void* out;               /* [sumT][out_ld]; may be logits itself (same type and ld) */
+  int64_t out_ld;
+  const int32_t* tree_off; /* [B+1] device                                       */
+  const int32_t* parent;   /* [sumT] device, nullable with token: no path tokens */
+  const int32_t* token;    /* [sumT] device                                      */
+  const int32_t* hist;     /* [B][hist_ld] committed tokens, nullable            */
+  int64_t hist_ld;
+  const int32_t* hist_len;     /* [B] device, with hist                          */
+  const int32_t* prompt_len;   /* [B] device, nullable (0: all of it was made)   */
+  const float* repetition;     /* [B] device, nullable (1); finite and > 0       */
+  const float* presence;       /* [B] device, nullable (0)                       */
+  const float* frequency;      /* [B] device, nullable (0)                       */
+  const int32_t* bias_off;     /* [B+1] device CSR, nullable: no biases          */
+  const int32_t* bias_token;   /* ascending without repeats within a request     */
+  const float* bias_value;
+  const uint32_t* allow;       /* [allow_rows][allow_ld] grammar masks, bit v%32 of word v/32;
+                                  nullable                                       */
+  int64_t allow_ld;            /* words between rows, >= ceil(V/32)              */
+  int32_t allow_rows;
+  const int32_t* allow_row;    /* [sumT] device: the node's row, negative = unconstrained;
+                                  NULL: row t                                    */
+  int32_t* d_err;              /* nullable. KDV_DERR_BAD_TOKEN: a history, path or
+                                  bias token outside [0, V) (that entry is left out), biases out of order
+                                  or repeated (which of them apply is unspecified), or an allow row >= allow_rows (unconstrained then);
+                                  KDV_DERR_BAD_PARENT (no path tokens for that request);
+                                  KDV_DERR_BAD_LENGTH: T_b outside [0, max_T], tree_off beyond
+                                  total_nodes, a length outside [0, hist_ld] (clamped);
+                                  KDV_DERR_BAD_SCORE: repetition not finite or <= 0 (1 is taken) */
+} kdv_logits_params;
+KDV_API kdv_status kdv_logits_process(const kdv_logits_params* p, void* stream);
 
 #ifdef __cplusplus
 }

@@ -52,13 +52,22 @@ KDV_IMPL_TC_1SM = 3          # retired: kdv_verify_attn returns KDV_ERR_UNSUPPOR
 KDV_IMPL_TC_STAGED = 4
 KDV_MAX_TREE = 64
 KDV_MAX_BATCH = 128
+KDV_ROPE_INTERLEAVED = 0
+KDV_ROPE_HALF = 1
+KDV_MAX_ROT = 256
+KDV_ROPE_SCALE_NONE = 0
+KDV_ROPE_SCALE_LINEAR = 1
+KDV_ROPE_SCALE_NTK = 2
+KDV_ROPE_SCALE_YARN = 3
 
 # Every entry point include/kdv.h declares (checked by the CPU tests).
 EXPORTED = ("kdv_status_string", "kdv_version", "kdv_tree_mask_build",
             "kdv_verify_attn_workspace", "kdv_verify_attn_plan", "kdv_verify_attn",
             "kdv_verify_attn_noalloc", "kdv_latent_f16", "kdv_combine", "kdv_tree_accept_workspace",
             "kdv_tree_accept", "kdv_absorb_q", "kdv_unabsorb_o", "kdv_tree_build",
-            "kdv_absorb_q_ex", "kdv_unabsorb_o_ex", "kdv_verify_attn_launches")
+            "kdv_absorb_q_ex", "kdv_unabsorb_o_ex", "kdv_verify_attn_launches",
+            "kdv_rope_freqs", "kdv_rope", "kdv_latent8_write", "kdv_verify_attn8_workspace",
+            "kdv_verify_attn8_plan", "kdv_verify_attn8", "kdv_logits_process")
 KDV_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -117,6 +126,67 @@ class BuildParams(ctypes.Structure):
     ]
 
 
+class RopeParams(ctypes.Structure):
+    """Mirror of ``kdv_rope_params`` (field order and types must match kdv.h)."""
+    _fields_ = [
+        ("tokens", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+        ("x", ctypes.c_void_p), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+        ("y", ctypes.c_void_p), ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64),
+        ("pos", ctypes.c_void_p), ("batch", ctypes.c_int32), ("tree_off", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p), ("depth", ctypes.c_void_p), ("h_inv_freq", ctypes.c_void_p),
+        ("mscale", ctypes.c_float),
+    ]
+
+
+class Latent8Params(ctypes.Structure):
+    """Mirror of ``kdv_latent8_params`` (field order and types must match kdv.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("d_latent", ctypes.c_int32), ("d_rope", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("c", ctypes.c_void_p), ("c_stride", ctypes.c_int64), ("k_rope", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+        ("slot", ctypes.c_void_p), ("batch", ctypes.c_int32), ("tree_off", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p), ("depth", ctypes.c_void_p), ("kv_off", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("h_inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32), ("mscale", ctypes.c_float), ("pos", ctypes.c_void_p),
+        ("c8", ctypes.c_void_p), ("kr", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("num_slots", ctypes.c_int64), ("scale_block", ctypes.c_int32), ("static_scale", ctypes.c_int32),
+        ("d_err", ctypes.c_void_p),
+    ]
+
+
+class Verify8Params(ctypes.Structure):
+    """Mirror of ``kdv_verify8_params`` (field order and types must match kdv.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("num_heads", ctypes.c_int32), ("d_latent", ctypes.c_int32),
+        ("d_rope", ctypes.c_int32), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32), ("impl", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64),
+        ("c8", ctypes.c_void_p), ("kr", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("scale_block", ctypes.c_int32), ("num_slots", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p), ("kv_off", ctypes.c_void_p), ("tree_off", ctypes.c_void_p),
+        ("prefix_len", ctypes.c_void_p), ("h_prefix_len", ctypes.POINTER(ctypes.c_int32)),
+        ("h_tree_T", ctypes.POINTER(ctypes.c_int32)), ("mask", ctypes.c_void_p), ("num_splits", ctypes.c_int32),
+        ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("d_err", ctypes.c_void_p), ("wait_limit_ns", ctypes.c_uint64),
+    ]
+
+
+class LogitsParams(ctypes.Structure):
+    """Mirror of ``kdv_logits_params`` (field order and types must match kdv.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("max_T", ctypes.c_int32), ("total_nodes", ctypes.c_int32),
+        ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("logits", ctypes.c_void_p), ("logits_ld", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_ld", ctypes.c_int64),
+        ("tree_off", ctypes.c_void_p), ("parent", ctypes.c_void_p), ("token", ctypes.c_void_p),
+        ("hist", ctypes.c_void_p), ("hist_ld", ctypes.c_int64), ("hist_len", ctypes.c_void_p),
+        ("prompt_len", ctypes.c_void_p), ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+        ("frequency", ctypes.c_void_p), ("bias_off", ctypes.c_void_p), ("bias_token", ctypes.c_void_p),
+        ("bias_value", ctypes.c_void_p), ("allow", ctypes.c_void_p), ("allow_ld", ctypes.c_int64),
+        ("allow_rows", ctypes.c_int32), ("allow_row", ctypes.c_void_p), ("d_err", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -168,6 +238,21 @@ def load() -> ctypes.CDLL:
         lib.kdv_unabsorb_o_ex.restype = c.c_int
         lib.kdv_tree_build.argtypes = [c.POINTER(BuildParams), c.c_void_p]
         lib.kdv_tree_build.restype = c.c_int
+        lib.kdv_rope_freqs.argtypes = [c.c_int32, c.c_double, c.c_int32, c.c_double, c.c_double, c.c_double,
+                                       c.c_double, c.c_void_p, c.POINTER(c.c_double)]
+        lib.kdv_rope_freqs.restype = c.c_int
+        lib.kdv_rope.argtypes = [c.POINTER(RopeParams), c.c_void_p]
+        lib.kdv_rope.restype = c.c_int
+        lib.kdv_latent8_write.argtypes = [c.POINTER(Latent8Params), c.c_void_p]
+        lib.kdv_latent8_write.restype = c.c_int
+        lib.kdv_verify_attn8_workspace.argtypes = [c.POINTER(Verify8Params), c.POINTER(c.c_size_t)]
+        lib.kdv_verify_attn8_workspace.restype = c.c_int
+        lib.kdv_verify_attn8_plan.argtypes = [c.POINTER(Verify8Params), c.c_void_p, c.c_void_p]
+        lib.kdv_verify_attn8_plan.restype = c.c_int
+        lib.kdv_verify_attn8.argtypes = [c.POINTER(Verify8Params), c.c_void_p]
+        lib.kdv_verify_attn8.restype = c.c_int
+        lib.kdv_logits_process.argtypes = [c.POINTER(LogitsParams), c.c_void_p]
+        lib.kdv_logits_process.restype = c.c_int
         if hasattr(lib, "kdv_trace_read"):          # the tracing build
             lib.kdv_trace_clear.argtypes = [c.c_void_p]
             lib.kdv_trace_clear.restype = c.c_int
@@ -334,6 +419,126 @@ def kdv_combine(o_part: torch.Tensor, lse_part: torch.Tensor, S: int, rows: int,
                 o: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None) -> None:
     _check(load().kdv_combine(_ptr(o_part), _ptr(lse_part), int(S), int(rows), int(d), _ptr(o),
                               _ptr(lse), _stream(stream)), "kdv_combine")
+
+
+# ---------------------------------------------------------------------------
+# The 8-bit latent cache, rotary positions and logits processing.
+# ---------------------------------------------------------------------------
+_FLOAT = (torch.bfloat16, torch.float32)
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+# fields of each kind, with the element types that a tensor given for them may have
+_FIELD_TYPES = {
+    **{f: _I32 for f in ("pos", "tree_off", "prefix_len", "depth", "slot", "kv_off", "page_table", "parent", "token",
+                         "hist", "hist_len", "prompt_len", "bias_off", "bias_token", "allow_row", "d_err")},
+    **{f: _F32 for f in ("kv_scale", "lse", "repetition", "presence", "frequency", "bias_value")},
+    **{f: _FLOAT for f in ("x", "y", "c", "k_rope", "q", "o", "logits", "out")},
+    "kr": (torch.bfloat16,), "c8": (torch.uint8, torch.float8_e4m3fn), "mask": (torch.int64, torch.uint64),
+    "allow": (torch.int32, torch.uint32), "workspace": (torch.uint8,),
+}
+_STRIDED = ("x", "y", "c", "k_rope", "q", "logits", "out", "hist", "allow")    # their strides are fields of their own
+
+
+def _fill(p, kw: dict):
+    """Fill a parameter struct: tensors become pointers (checked for device and
+    element type, kept alive with the struct), HOST arrays are copied."""
+    p._keep, p._device = [], None
+    for k, v in kw.items():
+        if k in ("h_prefix_len", "h_tree_T"):
+            arr = (ctypes.c_int32 * len(v))(*[int(x) for x in v])
+            p._keep.append(arr)
+            setattr(p, k, ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32)))
+        elif k == "h_inv_freq" and v is not None:
+            arr = np.array(v, dtype=np.float64)
+            p._keep.append(arr)
+            p.h_inv_freq = arr.ctypes.data
+        elif isinstance(v, torch.Tensor):
+            if not v.is_cuda:
+                raise ValueError(f"{k}: a CUDA tensor is wanted")
+            if p._device not in (None, v.device.index):
+                raise ValueError(f"{k}: tensors of one call are on one device")
+            if v.dtype not in _FIELD_TYPES[k]:
+                raise TypeError(f"{k}: unsupported dtype {v.dtype}")
+            if not (v.is_contiguous() or (k in _STRIDED and (v.dim() == 0 or v.stride(-1) == 1))):
+                raise ValueError(f"{k}: its elements have to be contiguous")
+            p._device = v.device.index
+            p._keep.append(v)
+            setattr(p, k, v.data_ptr())
+        else:
+            setattr(p, k, v)
+    return p
+
+
+def _launch(fn: str, p, stream) -> None:
+    """Call an entry point on the device of the struct's tensors."""
+    f = getattr(load(), fn)
+    dev = getattr(p, "_device", None)
+    if dev is None or dev == torch.cuda.current_device():
+        status = f(ctypes.byref(p), _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = f(ctypes.byref(p), _stream(stream))
+    _check(status, fn)
+
+
+def kdv_rope_freqs(rot_dim: int, base: float = 10000.0, rule: int = KDV_ROPE_SCALE_NONE, factor: float = 1.0,
+                   trained_len: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inverse frequencies as a float64 array, magnitude factor) for kdv_rope / kdv_latent8_write."""
+    freq, mscale = np.zeros(max(0, int(rot_dim) // 2), dtype=np.float64), ctypes.c_double(0.0)
+    _check(load().kdv_rope_freqs(int(rot_dim), float(base), int(rule), float(factor), float(trained_len),
+                                 float(beta_fast), float(beta_slow), freq.ctypes.data, ctypes.byref(mscale)),
+           "kdv_rope_freqs")
+    return freq, float(mscale.value)
+
+
+def make_rope_params(**kw) -> RopeParams:
+    """A RopeParams from keyword arguments (tensors become pointers; h_inv_freq is copied)."""
+    return _fill(RopeParams(), {"mscale": 1.0, **kw})
+
+
+def kdv_rope(params: RopeParams, stream=None) -> None:
+    _launch("kdv_rope", params, stream)
+
+
+def make_latent8_params(**kw) -> Latent8Params:
+    """A Latent8Params from keyword arguments (tensors become pointers; h_inv_freq is copied)."""
+    return _fill(Latent8Params(), {"mscale": 1.0, "scale_block": 1, **kw})
+
+
+def kdv_latent8_write(params: Latent8Params, stream=None) -> None:
+    _launch("kdv_latent8_write", params, stream)
+
+
+def make_verify8_params(**kw) -> Verify8Params:
+    """A Verify8Params from keyword arguments (tensors become pointers)."""
+    return _fill(Verify8Params(), {"scale_block": 1, **kw})
+
+
+def kdv_verify_attn8_workspace(params: Verify8Params) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().kdv_verify_attn8_workspace(ctypes.byref(params), ctypes.byref(n)), "kdv_verify_attn8_workspace")
+    return int(n.value)
+
+
+def kdv_verify_attn8_plan(params: Verify8Params):
+    """(splits per request, work items) that kdv_verify_attn8 would use."""
+    splits = (ctypes.c_int32 * max(1, params.batch))()
+    items = ctypes.c_int32(0)
+    _check(load().kdv_verify_attn8_plan(ctypes.byref(params), splits, ctypes.byref(items)), "kdv_verify_attn8_plan")
+    return [int(splits[i]) for i in range(params.batch)], int(items.value)
+
+
+def kdv_verify_attn8(params: Verify8Params, stream=None) -> None:
+    _launch("kdv_verify_attn8", params, stream)
+
+
+def make_logits_params(**kw) -> LogitsParams:
+    """A LogitsParams from keyword arguments (tensors become pointers)."""
+    return _fill(LogitsParams(), kw)
+
+
+def kdv_logits_process(params: LogitsParams, stream=None) -> None:
+    _launch("kdv_logits_process", params, stream)
 
 
 # ---------------------------------------------------------------------------

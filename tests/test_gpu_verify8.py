@@ -1,0 +1,293 @@
+"""Attention over the 8-bit latent cache against its 64-bit form. Every bound is
+plain8.Attn.answer's, counted before the first run: a logit's fp32 rounding, the
+numerators' (2^-9 where they are split into 8-bit terms), the stored partials'
+and the output type's."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_tree_verify_mla_b200 import kdv
+from tests import plain8
+
+pytestmark = pytest.mark.gpu
+i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")  # noqa: E731
+CODE = {torch.bfloat16: kdv.KDV_BF16, torch.float32: kdv.KDV_F32}
+SIMT, TC, AUTO = kdv.KDV_IMPL_SIMT, kdv.KDV_IMPL_TC, kdv.KDV_IMPL_AUTO
+
+
+class Run:
+    def __init__(self, case, impl=AUTO, out=torch.float32, splits=0, chain=False, **kw):
+        self.case, c = case, case
+        rows = int(c.tree_off[-1]) * c.H
+        self.q = c.q.cuda()
+        self.c8, self.kr, self.scale = torch.from_numpy(c.c8).cuda(), c.kr.cuda(), torch.from_numpy(c.scale).cuda()
+        self.o = torch.full((rows, c.D_c), 5.0, dtype=out, device="cuda")
+        self.lse = torch.full((rows,), 5.0, device="cuda")
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        m = np.array([x if x < 2 ** 63 else x - 2 ** 64 for x in c.masks], dtype=np.int64)
+        self.mask = None if chain else torch.from_numpy(m).cuda()
+        base = dict(batch=c.B, num_heads=c.H, d_latent=c.D_c, d_rope=c.D_r, scale=c.sm_scale, dtype=CODE[self.q.dtype], out_dtype=CODE[out],
+                    impl=impl, q=self.q, q_row_stride=0, c8=self.c8, kr=self.kr if c.D_r else None, kv_scale=self.scale, scale_block=c.block,
+                    num_slots=c.slots, page_table=i32(c.table) if c.table is not None else None, kv_off=i32(c.kv_off), tree_off=i32(c.tree_off),
+                    prefix_len=i32(c.prefix), h_prefix_len=c.prefix, h_tree_T=c.T, mask=self.mask, num_splits=splits, o=self.o, lse=self.lse,
+                    d_err=self.err)
+        self.p = kdv.make_verify8_params(**{**base, **kw})
+        n = kdv.kdv_verify_attn8_workspace(self.p)
+        self.ws = torch.full((max(16, n),), 0xA5, dtype=torch.uint8, device="cuda")
+        self.p.workspace, self.p.workspace_bytes = self.ws.data_ptr(), n
+
+    def go(self, stream=None):
+        kdv.kdv_verify_attn8(self.p, stream)
+        return self
+
+    def check(self, err=0, drop=None, rows=None):
+        o, lse, ob, lb = self.case.answer(drop=drop)
+        got, gl = self.o.double().cpu().numpy(), self.lse.double().cpu().numpy()
+        assert self.err.item() == err
+        rows = np.arange(len(o)) if rows is None else rows
+        got, gl, o, lse, ob, lb = got[rows], gl[rows], o[rows], lse[rows], ob[rows], lb[rows]
+        none = np.isneginf(lse)
+        assert np.array_equal(np.isneginf(gl), none)
+        assert np.all(got[none] == 0.0)
+        tol = ob + plain8.half_step(self.o.dtype) * (np.abs(o) + ob)
+        e = np.abs(got - o)
+        assert np.all(e <= tol), (float((e / np.maximum(tol, 1e-30)).max()), float(e.max()))
+        el = np.abs(gl[~none] - lse[~none])
+        assert np.all(el <= lb[~none]), float((el / lb[~none]).max())
+        return self
+
+
+def tree(T, seed=0, reach=3):
+    return plain8.random_tree(np.random.default_rng(seed), T, reach)
+
+
+@pytest.mark.parametrize("q_dtype,D_c,D_r", [("bf16", 512, 64), ("f32", 512, 64), ("f32", 32, 8), ("bf16", 7, 0), ("f32", 509, 63), ("bf16", 1, 1)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_simt_types_and_dims(q_dtype, D_c, D_r, paged):
+    c = plain8.Attn(D_c, [40, 0, 3], [tree(5), tree(1), tree(9, 2)], H=3, D_c=D_c, D_r=D_r, block=4, paged=paged, q_dtype=q_dtype)
+    Run(c, SIMT).go().check()
+    Run(c, SIMT, splits=3, out=torch.bfloat16).go().check()
+
+
+SHAPES = [
+    ([0], [1], 64), ([1], [1], 16), ([127], [1], 64), ([128], [1], 1), ([126, 127, 128, 129], [1, 1, 1, 1], 8),
+    ([300], [13], 64), ([5], [64], 5), ([700, 0, 33], [3, 64, 7], 16), ([1000], [2], 128), ([255], [16], 17),
+]
+
+
+@pytest.mark.parametrize("prefix,sizes,H", SHAPES)
+@pytest.mark.parametrize("paged,block", [(False, 1), (True, 1), (True, 16)])
+def test_shapes(prefix, sizes, H, paged, block):
+    c = plain8.Attn(sum(prefix) + H, prefix, [tree(T, i) for i, T in enumerate(sizes)], H, block=block, paged=paged)
+    Run(c).go().check()
+    Run(c, splits=1, out=torch.bfloat16).go().check()
+    Run(c, splits=3).go().check()
+
+
+def test_more_splits_than_tiles_and_repeats():
+    c = plain8.Attn(3, [200, 10], [tree(4), tree(2)], 32)
+    a = Run(c, splits=7).go().check()
+    first = a.o.clone()
+    a.o.zero_()
+    a.go()
+    assert torch.equal(a.o, first)                                    # the same bits again
+
+
+def test_chain_is_causal_and_single_tokens():
+    c = plain8.Attn(4, [77, 500], [list(range(-1, 5)), [-1]], 64)
+    a, b = Run(c, chain=True).go().check(), Run(c).go()
+    assert torch.equal(a.o, b.o)
+    c = plain8.Attn(5, [10], [list(range(-1, 63))], 4)
+    Run(c, chain=True).go().check()
+
+
+def test_rows_that_see_nothing():
+    """Empty masks: with a prefix the node sees it alone; without one its rows are empty."""
+    masks = [0, 0b10, 0, 0b1]
+    c = plain8.Attn(6, [0, 9], [[-1, 0], [-1, 0]], 64, masks=masks)
+    Run(c).go().check()
+    Run(c, splits=2).go().check()
+    c = plain8.Attn(7, [0], [tree(40)], 16, masks=[0] * 40)
+    r = Run(c).go().check()
+    assert torch.all(r.o == 0) and torch.all(torch.isneginf(r.lse))
+
+
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+def test_unseen_keys_never_reach_an_output(impl):
+    """NaN codes, NaN rope parts, NaN and infinite scales in slots that a row does not see change no bit of it."""
+    sizes, prefix, H = [6, 3], [130, 0], 64
+    trees = [[-1, 0, 0, 1, 1, 2], [-1, 0, 0]]
+    for what in ("codes", "rope", "scale_nan", "scale_inf"):
+        c = plain8.Attn(8, prefix, trees, H)
+        clean = Run(c, impl).go().check()
+        # node 3 of request 0 (seen by itself alone), and every slot that no request owns
+        node = int(c.table[c.kv_off[0] + prefix[0] + 3])
+        free = np.setdiff1d(np.arange(c.slots), c.table)
+        dirty = np.append(free, node)
+        if what == "codes":
+            c.c8[dirty] = 0x7F
+        elif what == "rope":
+            c.kr[torch.from_numpy(dirty)] = float("nan")
+        else:
+            c.scale[dirty] = np.nan if what == "scale_nan" else np.inf
+        r = Run(c, impl).go()
+        own = np.arange(3 * H, 4 * H)
+        rest = np.setdiff1d(np.arange(sum(sizes) * H), own)
+        assert torch.equal(r.o[rest], clean.o[rest]) and torch.equal(r.lse[rest], clean.lse[rest]), what
+        assert torch.isnan(r.o[own]).any(1).all() and torch.isnan(r.lse[own]).all(), what
+
+
+def test_query_that_is_not_finite_stays_in_its_row():
+    c = plain8.Attn(9, [200], [tree(3)], 64)
+    clean = Run(c).go().check()
+    for bad in (float("nan"), float("inf")):
+        r = Run(c)
+        r.q[70, 5] = bad
+        r.q[10, 550] = bad
+        r.go()
+        rest = [i for i in range(192) if i not in (70, 10)]
+        assert torch.equal(r.o[rest], clean.o[rest]) and torch.equal(r.lse[rest], clean.lse[rest])
+        assert torch.isnan(r.lse[[70, 10]]).all()
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_growing_logits_and_scales(splits):
+    """The reference maximum and the scale's unit move in every tile; then they fall again."""
+    c = plain8.Attn(10, [900], [tree(2)], 64, sharp=2.0)
+    order = np.arange(900)
+    at = c.table[order]
+    c.scale[at] = (2.0 ** -12 * 1.013 ** np.minimum(order, 900 - order)).astype(np.float32)
+    Run(c, splits=splits).go().check()
+    c.scale[at] = (2.0 ** -3 * 0.99 ** order).astype(np.float32)
+    Run(c, splits=splits).go().check()
+
+
+def test_a_sink_and_a_long_flat_tail():
+    """One key holds half of the weight; thousands of keys far below it hold the rest."""
+    c = plain8.Attn(11, [6000], [[-1]], 64)
+    c.q = c.q * 0.02
+    q = c.q.double().mean(0).numpy()
+    sink = int(c.table[0])
+    c.c8[sink] = plain8.codes((np.sign(q[:512]) * 400)[None], np.ones(1))[0]
+    c.q[:, :512] = torch.from_numpy(np.sign(q[:512]) * 0.09).to(c.q.dtype)
+    Run(c, splits=1).go().check()
+    Run(c).go().check()
+
+
+def test_zero_and_negative_scales():
+    """A scale of 0 makes a row of zeros; a negative one its mirror."""
+    c = plain8.Attn(12, [300], [tree(2)], 64)
+    c.scale[c.table[:100]] = 0.0
+    c.scale[c.table[100:200]] *= -1.0
+    Run(c).go().check()
+    c.scale[:] = 0.0
+    r = Run(c).go().check()
+    assert torch.all(r.o == 0)
+
+
+def test_zero_queries_and_tiny_and_huge_values():
+    c = plain8.Attn(13, [200], [tree(3)], 64)
+    c.q[:64] = 0.0
+    c.q[64:128] *= 2.0 ** -40
+    c.q[100] *= 2.0 ** 30
+    c.scale *= 2.0 ** -20
+    Run(c).go().check()
+
+
+def test_bad_slots_and_lengths():
+    c = plain8.Attn(14, [150, 40], [tree(3), tree(2)], 64)
+    good = Run(c).go().check()
+    table = c.table.copy()
+    lost = [int(table[5]), int(table[149])]
+    table[5], table[149] = c.slots, -7
+    Run(c, page_table=i32(table)).go().check(err=kdv.KDV_DERR_BAD_SLOT, drop=lost)
+    Run(c, page_table=i32(table), impl=SIMT).go().check(err=kdv.KDV_DERR_BAD_SLOT, drop=lost)
+    # a request whose range is too short has no keys; the other is whole
+    off = c.kv_off.copy()
+    off[1] -= 1
+    r = Run(c, kv_off=i32(np.array([off[0], off[1], off[1] + 200])), page_table=None, num_slots=c.slots)
+    r.go()
+    assert r.err.item() == kdv.KDV_DERR_BAD_LENGTH
+    assert torch.all(r.o[:192] == 0) and torch.all(torch.isneginf(r.lse[:192])) and torch.isfinite(r.lse[192:]).all()
+    r = Run(c, prefix_len=i32([150, 41])).go()
+    assert r.err.item() == kdv.KDV_DERR_BAD_LENGTH and torch.equal(r.o, good.o)
+
+
+def test_query_strides_and_nullable_outputs():
+    c = plain8.Attn(15, [100], [tree(2)], 64)
+    base = Run(c).go().check()
+    wide = torch.zeros(128, 640, dtype=torch.bfloat16, device="cuda")
+    wide[:, :576] = base.q
+    r = Run(c, q=wide, q_row_stride=640, lse=None, d_err=None).go()
+    assert torch.equal(r.o, base.o)
+    odd = torch.zeros(128, 577, dtype=torch.bfloat16, device="cuda")       # rows that are not 16-byte aligned
+    odd[:, :576] = base.q
+    Run(c, q=odd, q_row_stride=577).go().check()
+
+
+def test_rows_behind_the_last_request_stay():
+    c = plain8.Attn(16, [64], [tree(3)], 20)
+    rows = 60
+    o = torch.full((rows + 100, 512), 5.0, device="cuda")
+    lse = torch.full((rows + 100,), 5.0, device="cuda")
+    r = Run(c, o=o, lse=lse).go()
+    assert torch.all(o[rows:] == 5.0) and torch.all(lse[rows:] == 5.0)
+    r.o, r.lse = o[:rows], lse[:rows]
+    r.check()
+
+
+def test_slots_beyond_32_bit_offsets():
+    slots = 9_000_000
+    c = plain8.Attn(17, [300], [tree(2)], 16)
+    far = np.concatenate([np.arange(8_388_600, 8_388_600 + 150), np.arange(slots - 152, slots)])
+    c8 = torch.zeros(slots, 512, dtype=torch.uint8, device="cuda")
+    kr, scale = torch.zeros(slots, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(slots, device="cuda")
+    old = torch.from_numpy(c.table.astype(np.int64))
+    c8[far], kr[far], scale[far] = torch.from_numpy(c.c8)[old].cuda(), c.kr[old].cuda(), torch.from_numpy(c.scale)[old].cuda()
+    Run(c, c8=c8, kr=kr, kv_scale=scale, num_slots=slots, page_table=i32(far)).go().check()
+
+
+def test_streams_and_graphs_with_their_own_workspaces():
+    a, b = Run(plain8.Attn(18, [700], [tree(5)], 64)), Run(plain8.Attn(19, [500, 20], [tree(2), tree(9)], 32))
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (sa, sb):
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):                                                # two calls at once
+        a.go(sa)
+        b.go(sb)
+    for s in (sa, sb):
+        torch.cuda.current_stream().wait_stream(s)
+    a.check()
+    b.check()
+    want = a.o.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.go()
+        b.go()
+    a.o.zero_()
+    b.o.zero_()
+    a.ws.fill_(0xFF)
+    for _ in range(2):
+        graph.replay()
+    a.check()
+    b.check()
+    assert torch.equal(a.o, want)
+
+
+def test_writes_just_before_are_seen():
+    c = plain8.Attn(20, [400], [tree(4)], 64)
+    r = Run(c)
+    q, c8 = r.q.clone(), r.c8.clone()
+    for _ in range(3):
+        r.q.zero_()
+        r.c8.zero_()
+        r.go()
+        r.q.copy_(q)
+        r.c8.copy_(c8)
+        r.go()
+    r.check()
+
+
+def test_long_context():
+    c = plain8.Attn(21, [40000], [[-1]], 16, paged=False)
+    Run(c).go().check()
