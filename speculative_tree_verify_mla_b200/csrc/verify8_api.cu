@@ -34,7 +34,8 @@ bool tc_pointers(const kdv_verify8_params* p) {
 }
 
 int resolve(const kdv_verify8_params* p) {
-  return KDV_IMPL_SIMT;
+  if (p->impl != KDV_IMPL_AUTO) return p->impl;
+  return tc_shape(p) && tc_pointers(p) ? KDV_IMPL_TC : KDV_IMPL_SIMT;
 }
 
 kdv_status check(const kdv_verify8_params* p) {
@@ -53,7 +54,7 @@ kdv_status check(const kdv_verify8_params* p) {
     if (p->h_prefix_len[b] < 0 || p->h_tree_T[b] < 1) return KDV_ERR_INVALID_ARG;
     if (p->h_tree_T[b] > KDV_MAX_TREE || p->h_prefix_len[b] > INT_MAX / 2) return KDV_ERR_UNSUPPORTED;
   }
-  if (p->impl == KDV_IMPL_TC) return KDV_ERR_UNSUPPORTED;
+  if (p->impl == KDV_IMPL_TC && !tc_shape(p)) return KDV_ERR_UNSUPPORTED;
   const int64_t D_q = (int64_t)p->d_latent + p->d_rope;
   if (p->q_row_stride != 0 && p->q_row_stride < D_q) return KDV_ERR_INVALID_ARG;
   return KDV_OK;
@@ -222,7 +223,7 @@ kdv_status kdv_verify_attn8(const kdv_verify8_params* p, void* stream) {
     a.part_s = reinterpret_cast<float2*>(static_cast<char*>(p->workspace) + part_o_bytes(v, p->d_latent));
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_verify8_simt(a, v, s);
+  cudaError_t e = impl == KDV_IMPL_TC ? launch_verify8_tc(a, v, s) : launch_verify8_simt(a, v, s);
   if (e == cudaSuccess && v.out_mode == OUT_WORKSPACE) e = launch_combine8(a, v, s);
   return e == cudaSuccess ? KDV_OK : KDV_ERR_CUDA;
 }

@@ -150,6 +150,29 @@ def test_query_that_is_not_finite_stays_in_its_row():
         assert torch.isnan(r.lse[[70, 10]]).all()
 
 
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+def test_half_of_the_heads_not_finite(impl):
+    """Queries that are NaN for whole groups of 32 rows leave the other rows' bits alone."""
+    c = plain8.Attn(22, [200], [tree(2)], 64)
+    clean = Run(c, impl).go().check()
+    for lo in (0, 32):
+        r = Run(c, impl)
+        r.q[lo:lo + 32] = float("nan")
+        r.go()
+        rest = [i for i in range(128) if not lo <= i < lo + 32]
+        assert torch.equal(r.o[rest], clean.o[rest]) and torch.equal(r.lse[rest], clean.lse[rest])
+        assert torch.isnan(r.o[lo:lo + 32]).all() and torch.isnan(r.lse[lo:lo + 32]).all()
+
+
+def test_queries_over_the_whole_exponent_range():
+    """Rows of 2^100 and 2^-100 under scales that bring the logits back."""
+    for e in (100, -40):
+        c = plain8.Attn(23, [150], [tree(2)], 64)
+        c.q = c.q * 2.0 ** e
+        c.scale = (c.scale * 2.0 ** -e).astype(np.float32)
+        Run(c).go().check()
+
+
 @pytest.mark.parametrize("splits", [1, 3])
 def test_growing_logits_and_scales(splits):
     """The reference maximum and the scale's unit move in every tile; then they fall again."""
