@@ -61,9 +61,10 @@ constexpr int PARTS = 5;                     // blocks of a tile: rope, latent 0
 constexpr int RING = 7;
 constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;
 constexpr int KS_BUFS = 4;
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, PRODUCER_WARPS = 4;
+constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, PRODUCER_WARPS = 3;
 constexpr int THREADS = (SOFTMAX_WARPS + 1 + PRODUCER_WARPS) * 32;
 constexpr float P_TOP = 12.f, P_GROW = 15.f; // log2 of the largest p when the reference is set / allowed later
+constexpr float UNIT_ROOM = 4.f;             // how far scales may grow before their unit moves
 constexpr float NO_MAX = -1e30f;             // the reference of a row that has seen no key
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
@@ -95,6 +96,14 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
       :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
 }
+// One lane of a converged warp, the same at every call. The issuing warp runs
+// its loop with all lanes and elects around each block of MMAs: measured 48 clocks an
+// N = 64 MMA, 69 with a predicate on each (which is what their operands take to read: 46).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // kind::f8f6f4 with fp32 D: formats 0 e4m3, 1 e5m2
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_fmt, int b_fmt, bool a_mn, bool b_mn) {
   return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
@@ -119,7 +128,8 @@ __device__ __forceinline__ uint64_t global_ns() {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // Bounded waits: a wait that runs out reports, raises the CTA's abort flag and
 // returns false; from then on every other wait of the CTA returns at once.
@@ -152,7 +162,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-// largest |x| of a warp / largest x, through the order-preserving integer image of a float
+__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// largest x of a warp, through the order-preserving integer image of a float
 __device__ __forceinline__ float warp_max(float x) {
   int i = __float_as_int(x);
   i ^= (i >> 31) & 0x7fffffff;
@@ -162,55 +177,87 @@ __device__ __forceinline__ float warp_max(float x) {
 
 // ------------------------------------------------------------------ queries
 // One row by one warp: lane l holds latent elements 16 l .. 16 l + 15 and rope
-// elements 2 l, 2 l + 1. Returns the row's logit factor scale log2(e) 2^-k.
-__device__ __forceinline__ float stage_query(const Verify8Args& a, const __nv_bfloat16* row, bool valid, int r, uint8_t* sp, int lane) {
-  float v[16];
-  uint32_t rope = 0;
-  if (valid) {
-    const uint4 w0 = reinterpret_cast<const uint4*>(row)[2 * lane], w1 = reinterpret_cast<const uint4*>(row)[2 * lane + 1];
-    const uint32_t u[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// elements 2 l, 2 l + 1.
+struct QueryRow {
+  uint32_t u[8], rope;
+  __device__ __forceinline__ void load(const __nv_bfloat16* row, bool valid, int lane) {
+    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+    rope = 0;
+    if (valid) {
+      w0 = reinterpret_cast<const uint4*>(row)[2 * lane];
+      w1 = reinterpret_cast<const uint4*>(row)[2 * lane + 1];
+      rope = reinterpret_cast<const uint32_t*>(row + DC)[lane];
     }
-    rope = reinterpret_cast<const uint32_t*>(row + DC)[lane];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    u[0] = w0.x; u[1] = w0.y; u[2] = w0.z; u[3] = w0.w;
+    u[4] = w1.x; u[5] = w1.y; u[6] = w1.z; u[7] = w1.w;
   }
-  float top = 0.f;
+  // Writes the row's terms; returns its logit factor scale log2(e) 2^-k.
+  __device__ __forceinline__ float stage(float scale, int r, uint8_t* sp, int lane) const {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = fmaxf(top, finite(v[i]) ? fabsf(v[i]) : 0.f);
-  top = warp_max(top);
-  // the power of two that brings the largest element into [128, 256)
-  int e = top > 0.f ? 7 - ilogbf(top) : 0;
-  e = max(-120, min(60, e));
-  const float up = ldexpf(1.f, e);
-  uint32_t hi[4], lo[4];
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
+    uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    const bool bad = top >= 0x7f80u;               // an infinity or a NaN in the row (warp-uniform)
+    if (bad) {
+      m = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x[4], y[4];
-    uint32_t h = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = finite(v[4 * i + j]) ? v[4 * i + j] * up : __int_as_float(0x7fc00000);
-    h = e4m3x4(x[0], x[1], x[2], x[3]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      __nv_fp8_e4m3 t;
-      t.__x = (uint8_t)(h >> (8 * j));
-      y[j] = isnan(x[j]) ? 0.f : 16.f * (x[j] - (float)t);   // the low terms stay finite, see the softmax
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t lo = u[i] & 0x7fffu, hi = (u[i] >> 16) & 0x7fffu;
+        m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+      top = __reduce_max_sync(0xffffffffu, m);
     }
-    hi[i] = h;
-    lo[i] = e4m3x4(y[0], y[1], y[2], y[3]);
+    // the power of two that brings the largest element into [128, 256)
+    const int e = top == 0u ? 0 : max(-120, min(60, 7 + 127 - (int)(top >> 7)));
+    const float up = __int_as_float((e + 127) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[4], y[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[2 * j] = __uint_as_float(u[2 * i + j] << 16) * up;
+        x[2 * j + 1] = __uint_as_float(u[2 * i + j] & 0xffff0000u) * up;
+      }
+      if (bad) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = finite(x[j]) ? x[j] : __int_as_float(0x7fc00000);
+      }
+      hi[i] = e4m3x4(x[0], x[1], x[2], x[3]);
+      const float2 h01 = e4m3x2_values(hi[i] & 0xffffu), h23 = e4m3x2_values(hi[i] >> 16);
+      y[0] = 16.f * (x[0] - h01.x);
+      y[1] = 16.f * (x[1] - h01.y);
+      y[2] = 16.f * (x[2] - h23.x);
+      y[3] = 16.f * (x[3] - h23.y);
+      if (bad) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = isnan(y[j]) ? 0.f : y[j];   // the low terms stay finite, see the softmax
+      }
+      lo[i] = e4m3x4(y[0], y[1], y[2], y[3]);
+    }
+    const uint32_t blk = (uint32_t)(lane / 8) * BLOCK, col = (uint32_t)(lane % 8) * 16;
+    *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    const float ra = __uint_as_float(rope << 16) * up, rb = __uint_as_float(rope & 0xffff0000u) * up;
+    *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = pack_bf16x2(ra, rb);
+    *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
+    return fminf(fmaxf(scale * LOG2E * __int_as_float((127 - e) << 23), 1.17549435e-38f), 3.402823466e38f);
   }
-  const uint32_t blk = (uint32_t)(lane / 8) * BLOCK, col = (uint32_t)(lane % 8) * 16;
-  *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  const float ra = __uint_as_float(rope << 16) * up, rb = __uint_as_float(rope & 0xffff0000u) * up;
-  *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = pack_bf16x2(ra, rb);
-  *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
-  return fminf(fmaxf(a.scale * LOG2E * ldexpf(1.f, -e), 1.17549435e-38f), 3.402823466e38f);
+};
+
+// Reduction of 32 values a lane over the warp's lanes: halves of the rows swap
+// sides, so that lane r ends with row r (31 shuffles where a reduction per row takes 32 times five).
+template <typename F> __device__ __forceinline__ float transpose_reduce(float (&v)[32], int lane, F join) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const float keep = up ? v[k + o] : v[k], send = up ? v[k] : v[k + o];
+      v[k] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  return v[0];
 }
 
 // Two fp16 numerators -> their three e5m2 terms: the upper bytes of the first
@@ -287,7 +334,12 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       }
     };
     int next[4];
-    int n = warp - MMA_WARP - 1;
+    int n = warp - MMA_WARP - 1, pending = -1;       // pending: the ring place whose rows are in flight
+    auto arrive = [&]() {                            // all but the last group have landed
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_FULL + pending));
+    };
     load_slots(n / PARTS, next);
     for (; n < NT * PARTS; n += PRODUCER_WARPS) {
       const int tile = n / PARTS, part = n % PARTS, pos = n % RING, use = n / RING;
@@ -295,21 +347,30 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 #pragma unroll
       for (int g = 0; g < 4; ++g) slot[g] = next[g];
       load_slots((n + PRODUCER_WARPS) / PARTS, next);
-      if (use > 0 && !__all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1))) break;
+      if (use > 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar(B_EMPTY + pos), (use - 1) & 1))) {
+        if (pending >= 0) {                          // nothing to add yet: hand over what is in flight
+          cp_async_wait<0>();
+          arrive();
+          pending = -1;
+        }
+        if (!__all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1))) break;
+      }
       const uint32_t dst = base + OFF_RING + pos * BLOCK;
       const int sub = lane >> 3, col = (lane & 7) * 16;
+      const uint8_t* src0 = part == 0 ? reinterpret_cast<const uint8_t*>(a.kr) + col : a.c8 + (part - 1) * 128 + col;
+      const int64_t pitch = part == 0 ? DR * 2 : DC;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        int s[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[q] = __shfl_sync(0xffffffffu, slot[g], q * 4 + sub);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const int row = g * 32 + q * 4 + sub;
-          const int s = __shfl_sync(0xffffffffu, slot[g], q * 4 + sub);
-          const int64_t at = s < 0 ? 0 : s;
-          const uint8_t* src = part == 0 ? reinterpret_cast<const uint8_t*>(a.kr) + at * (DR * 2) + col
-                                         : a.c8 + at * DC + (part - 1) * 128 + col;
-          cp_async16(dst + swz128(row * 128 + col), src, s < 0 ? 0 : 16);
+          cp_async16(dst + swz128(row * 128 + col), src0 + (s[q] < 0 ? 0 : s[q]) * pitch, s[q] < 0 ? 0 : 16);
         }
       }
+      cp_async_commit();
       if (part == 0) {
         float* ks = reinterpret_cast<float*>(sp + OFF_KS) + (tile % KS_BUFS) * KEYS;
         uint32_t* okw = reinterpret_cast<uint32_t*>(sp + OFF_OK) + (tile % KS_BUFS) * 4;
@@ -324,78 +385,97 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_KS + tile % KS_BUFS));
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_FULL + pos));
+      if (pending >= 0) {
+        cp_async_wait<1>();
+        arrive();
+      }
+      pending = pos;
     }
-    cp_async_wait_all();
+    cp_async_wait<0>();
+    if (pending >= 0) arrive();
   } else if (warp == MMA_WARP) {
     // ---------------------------------------------------------- MMA issue
-    if (lane == 0 && NT > 0) {
-      const uint32_t qb = base + OFF_Q, qr = base + OFF_QR, pb = base + OFF_P, ring = base + OFF_RING;
-      // Q.K^T of block n (its barrier has been waited for)
-      auto qk = [&](int n) {
-        const int tile = n / PARTS, part = n % PARTS, pos = n % RING;
-        const uint32_t kb = ring + pos * BLOCK, d = tmem + TM_S + (tile & 1) * 128;
+    if (NT > 0) {
+      const uint64_t q_desc = sw128_desc(base + OFF_Q, 16, 1024), qr_desc = sw128_desc(base + OFF_QR, 16, 1024);
+      const uint64_t p_desc = sw64_desc(base + OFF_P, P_BYTES, 512);
+      const uint64_t k_desc = sw128_desc(base + OFF_RING, 16, 1024), v_desc = sw128_desc(base + OFF_RING, BLOCK, 1024);
+      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+      int tile = 0, part = 0, pos = 0, use = 0;      // the next block of Q.K^T
+      auto ready = [&]() { return all(mbar_test_wait(bar(B_FULL + pos), use & 1)); };
+      // Q.K^T of that block (its barrier has been waited for)
+      auto qk = [&]() {
+        const uint64_t kb = k_desc + (uint32_t)(pos * (BLOCK / 16));
+        const uint32_t d = tmem + TM_S + (tile & 1) * 128;
+        bool good = true;
         tc_fence_after();
         if (part == 0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ss(d, sw128_desc(kb + k * 32, 16, 1024), sw128_desc(qr + k * 32, 16, 1024), IDESC_ROPE, k > 0);
-          tc_commit(bar(B_EMPTY + pos));
           // products of two kinds into one accumulator: the second kind waits
           // for the first (it has the softmax's time for that)
-          tc_commit(bar(B_ROPE));
-          return wait(bar(B_ROPE), tile & 1);
-        }
+          if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_f8(d, sw128_desc(kb + k * 32, 16, 1024), sw128_desc(qb + (part - 1) * BLOCK + k * 32, 16, 1024), IDESC_QK, 1u);
-        return true;
+            for (int k = 0; k < 4; ++k) mma_ss(d, kb + 2 * k, qr_desc + 2 * k, IDESC_ROPE, k > 0);
+            tc_commit(bar(B_EMPTY + pos));
+            tc_commit(bar(B_ROPE));
+          }
+          __syncwarp();
+          good = all(wait(bar(B_ROPE), tile & 1));
+        } else {
+          const uint64_t qb = q_desc + (uint32_t)((part - 1) * (BLOCK / 16));
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f8(d, kb + 2 * k, qb + 2 * k, IDESC_QK, 1u);
+          }
+          __syncwarp();
+        }
+        if (++part == PARTS) {
+          part = 0;
+          ++tile;
+        }
+        if (++pos == RING) {
+          pos = 0;
+          ++use;
+        }
+        return good;
       };
-      bool go = wait(bar(B_Q), 0);
-      int n = 0;                                     // next block of Q.K^T
+      bool go = all(wait(bar(B_Q), 0));
+      int vpos = 1;                                  // ring place of the next latent block of P.V
       for (int i = -1; i < NT && go; ++i) {
         if (i >= 0) {
           // the next tile's blocks while this tile's numerators are not ready;
           // the ring holds up to its third
-          const int most = (i + 1 < NT) ? (i + 1) * PARTS + 3 : n;
-          while (n < most && go && !mbar_test_wait(bar(B_P), i & 1)) {
-            if (mbar_test_wait(bar(B_FULL + n % RING), (n / RING) & 1)) {
-              go = qk(n);
-              ++n;
-            } else if (*abort) {
-              go = false;
-            }
+          while (tile == i + 1 && tile < NT && part < 3 && go && !all(mbar_test_wait(bar(B_P), i & 1))) {
+            if (ready()) go = qk();
+            else if (all(*abort != 0)) go = false;
           }
-          if (!go || !(go = wait(bar(B_P), i & 1))) break;
+          if (!go || !(go = all(wait(bar(B_P), i & 1)))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int mt = 0; mt < 4; ++mt) {
-            const int pos = (i * PARTS + 1 + mt) % RING;
-            const uint32_t vb = ring + pos * BLOCK;
+            const uint64_t vb = v_desc + (uint32_t)(vpos * (BLOCK / 16));
+            if (elect_one()) {
 #pragma unroll
-            for (int t = 0; t < TERMS; ++t)
+              for (int t = 0; t < TERMS; ++t)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f8(tmem + mt * 64, sw128_desc(vb + k * 4096, BLOCK, 1024), sw64_desc(pb + t * P_BYTES + k * 2048, P_BYTES, 512),
-                       IDESC_PV, (i > 0 || t > 0 || k > 0) ? 1u : 0u);
-            tc_commit(bar(B_EMPTY + pos));
+                for (int k = 0; k < 4; ++k)
+                  mma_f8(tmem + mt * 64, vb + k * 256, p_desc + (t * P_BYTES + k * 2048) / 16, IDESC_PV,
+                         (t > 0 || k > 0) ? 1u : (uint32_t)(i > 0));
+              tc_commit(bar(B_EMPTY + vpos));
+            }
+            __syncwarp();
+            vpos = vpos + 1 == RING ? 0 : vpos + 1;
           }
+          vpos = vpos + 1 == RING ? 0 : vpos + 1;    // over the rope block
         }
         if (i + 1 < NT) {
-          const int end = (i + 2) * PARTS;
-          while (n < end && go) {
-            go = wait(bar(B_FULL + n % RING), (n / RING) & 1) && qk(n);
-            ++n;
-          }
-          if (go) tc_commit(bar(B_S + ((i + 1) & 1)));
+          while (tile == i + 1 && go) go = all(wait(bar(B_FULL + pos), use & 1)) && qk();
+          if (go && elect_one()) tc_commit(bar(B_S + ((i + 1) & 1)));
+          __syncwarp();
         }
       }
       // nothing of this CTA may still run when its tensor memory is given
       // back: a wait of its own, whatever happened before
-      tc_commit(bar(B_FIN));
+      if (elect_one()) tc_commit(bar(B_FIN));
+      __syncwarp();
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(bar(B_FIN), 0) && global_ns() - t0 < TIMEOUT_NS) {}
     }
@@ -410,15 +490,24 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     float* red2 = reinterpret_cast<float*>(sp + OFF_RED2) + g * 4;
     const uint32_t wg_bar = 1 + g;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-    for (int r = warp; r < ROWS; r += SOFTMAX_WARPS) {
-      const int lr = r0 + r;
-      const bool valid = lr < rows_b;
-      const float c = stage_query(a, q + ((int64_t)p.tree_base[b] * p.H + lr) * a.q_row_stride, valid, r, sp, lane);
-      if (lane == 0) {
-        float* f = reinterpret_cast<float*>(cm + r / 2) + (r & 1);
-        f[0] = c;
-        f[2] = -NO_MAX;
-        rmask[r] = valid ? node_mask(a, p, b, lr / p.H) : 0ull;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {                    // four rows' loads in flight
+      QueryRow row[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int lr = r0 + warp + SOFTMAX_WARPS * (4 * h + k);
+        row[k].load(q + ((int64_t)p.tree_base[b] * p.H + lr) * a.q_row_stride, lr < rows_b, lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = warp + SOFTMAX_WARPS * (4 * h + k), lr = r0 + r;
+        const float c = row[k].stage(a.scale, r, sp, lane);
+        if (lane == 0) {
+          float* f = reinterpret_cast<float*>(cm + r / 2) + (r & 1);
+          f[0] = c;
+          f[2] = -NO_MAX;
+          rmask[r] = lr < rows_b ? node_mask(a, p, b, lr / p.H) : 0ull;
+        }
       }
     }
     fence_proxy_async_smem();
@@ -446,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       tc_fence_after();
       float t[32];
       bool dirty;
-      {
+      auto scores = [&]() {                          // t = s_j (q . k), -inf where the row does not see the key
         uint32_t hi[32], lo[32];
         const uint32_t sb = tmem + quarter + TM_S + (i & 1) * 128 + 32 * g;
         tmem_ld32(sb, hi);
@@ -454,8 +543,34 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         tmem_wait_ld();
         dirty = isnan(__uint_as_float(lo[0]));
 #pragma unroll
-        for (int r = 0; r < 32; ++r) t[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
-      }
+        for (int r = 0; r < 32; r += 2) {
+          float2 x = fma_f32x2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), make_float2(0.0625f, 0.0625f),
+                               make_float2(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
+          x = mul_f32x2(x, make_float2(s, s));
+          t[r] = x.x;
+          t[r + 1] = x.y;
+        }
+        if (!plain) {
+#pragma unroll
+          for (int r = 0; r < 32; ++r) {
+            const bool vis = readable && (u < 0 || ((rmask[32 * g + r] >> u) & 1ull));
+            t[r] = vis ? t[r] : -INFINITY;
+          }
+        }
+      };
+      auto exponents = [&]() {                       // t = log2 of the numerators; the largest
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < 32; r += 2) {
+          const float4 f = cm[16 * g + r / 2];
+          const float2 d = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+          t[r] = d.x;
+          t[r + 1] = d.y;
+          top = fmaxf(top, fmaxf(d.x, d.y));
+        }
+        return top;
+      };
+      scores();
       // The low terms of a query are finite whatever the query holds, so a NaN
       // in their sums is the key's: its row of V becomes zeros, or 0 * NaN would
       // reach rows that do not see it. (Rows that see it get their NaN from p.)
@@ -466,39 +581,21 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
         }
       }
-      if (plain) {
-#pragma unroll
-        for (int r = 0; r < 32; ++r) t[r] *= s;
-      } else {
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          const bool vis = readable && (u < 0 || ((rmask[32 * g + r] >> u) & 1ull));
-          t[r] = vis ? t[r] * s : -INFINITY;
-        }
-      }
-      bool move = fabsf(s) > unit;
-#pragma unroll
-      for (int r = 0; r < 32; r += 2) {
-        const float4 f = cm[16 * g + r / 2];
-        const float2 d = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-        move |= fmaxf(d.x, d.y) > P_GROW;
-      }
+      const bool move = exponents() > P_GROW || fabsf(s) > unit;
       if (named_bar_or(wg_bar, 128, move)) {
         // ---- some reference moves: maxima over the tile's keys, per row
-        float mine = 0.f;                            // of row `lane`
+        scores();
 #pragma unroll
         for (int r = 0; r < 32; ++r) {
           const float4 f = cm[16 * g + r / 2];
-          float x = t[r] * ((r & 1) ? f.y : f.x);
-          x = isnan(x) ? -INFINITY : x;
-          const float top = warp_max(x);
-          if (lane == r) mine = top;
+          t[r] *= (r & 1) ? f.y : f.x;
         }
+        const float mine = transpose_reduce(t, lane, [](float x, float y) { return fmaxf(x, y); });   // of row `lane`
         red[w * 32 + lane] = mine;
         const float smax = warp_max(isnan(s) ? 0.f : fabsf(s));
         if (lane == 0) red2[w] = smax;
         named_bar_sync(wg_bar, 128);
-        const float top = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));
+        const float top = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));   // NaN: no key moves it
         const float st = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
         float* cr = reinterpret_cast<float*>(cm + 16 * g + lane / 2) + (lane & 1);
         const float m_old = -cr[2];
@@ -507,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         if (st > unit) {
           int e;
           const float m = frexpf(st, &e);
-          unit_new = ldexpf(1.f, max(m == 0.5f ? e - 1 : e, -120));
+          unit_new = UNIT_ROOM * ldexpf(1.f, max(m == 0.5f ? e - 1 : e, -120));
         } else if (unit == 0.f) {
           unit_new = ldexpf(1.f, -120);              // scales of 0 so far
         }
@@ -536,6 +633,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
           }
           tmem_wait_st();
         }
+        scores();
+        exponents();
       }
       const float sr = s * inv_unit;
 #pragma unroll
@@ -547,17 +646,16 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int r = 16 * h + 4 * q4 + 2 * k;
-            const float4 f = cm[16 * g + r / 2];
-            const float2 d = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-            const float p0 = ex2(d.x), p1 = ex2(d.y);
-            l[r] += p0;
-            l[r + 1] += p1;
-            float e0 = p0 * sr, e1 = p1 * sr;
+            const float p0 = ex2(t[r]), p1 = ex2(t[r + 1]);
+            const float2 sum = add_f32x2(make_float2(l[r], l[r + 1]), make_float2(p0, p1));
+            l[r] = sum.x;
+            l[r + 1] = sum.y;
+            float2 e = mul_f32x2(make_float2(p0, p1), make_float2(sr, sr));
             if (!plain) {                            // an unseen key's scale may be NaN
-              e0 = p0 == 0.f ? 0.f : e0;
-              e1 = p1 == 0.f ? 0.f : e1;
+              e.x = p0 == 0.f ? 0.f : e.x;
+              e.y = p1 == 0.f ? 0.f : e.y;
             }
-            split_p(pack_f16x2(e0, e1), t0[k], t1[k], t2[k]);
+            split_p(pack_f16x2(e.x, e.y), t0[k], t1[k], t2[k]);
           }
           w0[q4] = __byte_perm(t0[0], t0[1], 0x7531);
           w1[q4] = __byte_perm(t1[0], t1[1], 0x7531);
@@ -574,16 +672,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       if (lane == 0) mbar_arrive(bar(B_P));
     }
 
-    // ---- row sums over the 128 lanes: halves of the rows swap sides, so lane r ends with row r
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const bool up = (lane & o) != 0;
-#pragma unroll
-      for (int k = 0; k < o; ++k) {
-        const float keep = up ? l[k + o] : l[k], send = up ? l[k] : l[k + o];
-        l[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-      }
-    }
+    // ---- row sums over the 128 lanes
+    transpose_reduce(l, lane, [](float x, float y) { return x + y; });
     named_bar_sync(wg_bar, 128);
     red[w * 32 + lane] = l[0];
     named_bar_sync(wg_bar, 128);
@@ -605,10 +695,16 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     named_bar_sync(wg_bar, 128);
     if (NT > 0) wait(bar(B_FIN), 0);
     tc_fence_after();
+    // Output: lanes are dims and columns rows, so a block of 128 dims goes
+    // through shared memory (the ring is free) and leaves in 16-byte pieces of rows.
     const int64_t orow0 = out_row_index(p, b, split, r0 + 32 * g);
     const int nr = min(32, rows_b - r0 - 32 * g);
+    const bool wide = direct && a.out_f32;
+    const uint32_t line = wide ? 512 : 256;          // bytes of a row's 128 dims
+    uint8_t* out = static_cast<uint8_t*>(direct ? a.o : a.part_o);
 #pragma unroll 1
     for (int mt = 0; mt < 4; ++mt) {
+      uint8_t* stage = sp + OFF_RING + (2 * g + (mt & 1)) * BLOCK;
       uint32_t o[32];
       if (NT > 0) {
         tmem_ld32(tmem + quarter + mt * 64 + 32 * g, o);
@@ -617,16 +713,20 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 #pragma unroll
         for (int r = 0; r < 32; ++r) o[r] = 0u;
       }
-      const int dim = mt * 128 + w * 32 + lane;
 #pragma unroll
       for (int r = 0; r < 32; ++r) {
-        if (r >= nr) break;
         const float f = fac[32 * g + r];
         const float v = f == 0.f ? 0.f : __uint_as_float(o[r]) * f;
-        const int64_t at = (orow0 + r) * DC + dim;
-        if (!direct) static_cast<__half*>(a.part_o)[at] = __float2half_rn(v);
-        else if (a.out_f32) static_cast<float*>(a.o)[at] = v;
-        else static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v);
+        uint8_t* at = stage + r * line;
+        if (wide) reinterpret_cast<float*>(at)[key] = v;
+        else if (direct) reinterpret_cast<__nv_bfloat16*>(at)[key] = __float2bfloat16_rn(v);
+        else reinterpret_cast<__half*>(at)[key] = __float2half_rn(v);
+      }
+      named_bar_sync(wg_bar, 128);                   // the other buffer's readers have passed the barrier before this one
+      const int per = (int)line / 16;
+      for (int x = key; x < nr * per; x += 128) {
+        const int r = x / per, c = (x - r * per) * 16;
+        *reinterpret_cast<uint4*>(out + ((orow0 + r) * 4 + mt) * line + c) = *reinterpret_cast<const uint4*>(stage + r * line + c);
       }
     }
     tc_fence_before();
