@@ -155,62 +155,110 @@ __global__ void __launch_bounds__(WARPS * 32) verify8_simt_kernel(const __grid_c
 }
 
 // Merge of a request's split partials: LSE = ln sum_k exp(lse_k), o = sum_k
-// exp(lse_k - LSE) unit_k o_k. One warp a row, each lane two neighbouring
-// dims of every 64, so a warp reads 128 (fp16) or 256 bytes at a time. Reads
-// S * rows * D_c partials that the attention kernel has just left in L2.
+// exp(lse_k - LSE) unit_k o_k. Reads S * rows * D_c partials that the attention
+// kernel has just left in L2, so it is a matter of loads in flight: one CTA a
+// row, a thread holds four neighbouring dims and reads eight parts at a time;
+// the parts' weights are formed once, 128 of them at a time, in shared memory.
+constexpr int MERGE_THREADS = 128;
 template <typename TP>
-__global__ void __launch_bounds__(256) combine8_kernel(const __grid_constant__ Verify8Args a,
-                                                       const __grid_constant__ VerifyPlan p) {
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= p.total_rows) return;
+__global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_constant__ Verify8Args a,
+                                                                 const __grid_constant__ VerifyPlan p) {
+  __shared__ float weight[MERGE_THREADS];
+  __shared__ float red[2][MERGE_THREADS / 32];
+  const int tid = threadIdx.x, row = blockIdx.x, D = a.D_c;
   int b = 0;
   while (b + 1 < p.B && p.tree_base[b + 1] * p.H <= row) ++b;
   const int rows_b = p.T[b] * p.H, r = row - p.tree_base[b] * p.H, S = p.S[b];
   const int64_t base = p.part_base[b] + r;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the attention kernel's parts
   float m = -INFINITY;
   bool bad = false;                       // a NaN part makes the row NaN
-  for (int k = lane; k < S; k += 32) {
+  for (int k = tid; k < S; k += MERGE_THREADS) {
     const float l = a.part_s[base + (int64_t)k * rows_b].x;
     bad |= isnan(l);
     m = fmaxf(m, l);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (__any_sync(0xffffffffu, bad)) m = __int_as_float(0x7fc00000);
-  float sum = 0.f;
-  for (int k = lane; k < S; k += 32) {
-    const float l = a.part_s[base + (int64_t)k * rows_b].x;
-    sum += l == -INFINITY ? 0.f : expf(l - m);
+  if (__any_sync(0xffffffffu, bad)) m = INFINITY;          // lse is never +inf otherwise
+  if (tid % 32 == 0) red[0][tid / 32] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  if (m == INFINITY) m = __int_as_float(0x7fc00000);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  const TP* part = static_cast<const TP*>(a.part_o);
+  const int d0 = 4 * tid;                                  // D_c <= 512
+  const bool whole = D % 4 == 0;
+  for (int k0 = 0; k0 < S; k0 += MERGE_THREADS) {
+    const int n = min(MERGE_THREADS, S - k0);
+    if (k0 > 0) __syncthreads();
+    if (tid < n) {
+      const float2 su = a.part_s[base + (int64_t)(k0 + tid) * rows_b];
+      const float e = su.x == -INFINITY ? 0.f : expf(su.x - m);
+      sum += e;
+      weight[tid] = e * su.y;
+    }
+    __syncthreads();
+    if (d0 >= D) continue;
+    const TP* src = part + (base + (int64_t)k0 * rows_b) * D + d0;
+    const int64_t step = (int64_t)rows_b * D;
+    for (int k = 0; k < n; k += 8) {
+      float v[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
+        if (k + j >= n) continue;
+        if (whole) {
+          if constexpr (sizeof(TP) == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(src + j * step);
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+            v[j][0] = x.x; v[j][1] = x.y; v[j][2] = y.x; v[j][3] = y.y;
+          } else {
+            const float4 w = *reinterpret_cast<const float4*>(src + j * step);
+            v[j][0] = w.x; v[j][1] = w.y; v[j][2] = w.z; v[j][3] = w.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) if (d0 + i < D) v[j][i] = (float)src[j * step + i];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float w = k + j < n ? weight[k + j] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(w, v[j][i], acc[i]);
+      }
+      src += 8 * step;
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tid % 32 == 0) red[1][tid / 32] = sum;
+  __syncthreads();
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   const bool none = m == -INFINITY;
   const float inv = none ? 0.f : 1.f / sum;
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m + logf(sum);
-  const TP* part = static_cast<const TP*>(a.part_o);
-  for (int d0 = 0; d0 < a.D_c; d0 += 512) {
-    float acc[16];
+  if (tid == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m + logf(sum);
+  if (d0 >= D) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-    for (int k = 0; k < S; ++k) {
-      const float2 su = a.part_s[base + (int64_t)k * rows_b];
-      if (su.x == -INFINITY) continue;
-      const float w = expf(su.x - m) * inv * su.y;
-      const TP* src = part + (base + (int64_t)k * rows_b) * a.D_c;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int d = d0 + 64 * i + 2 * lane;
-        if (d < a.D_c) acc[2 * i] = fmaf(w, (float)src[d], acc[2 * i]);
-        if (d + 1 < a.D_c) acc[2 * i + 1] = fmaf(w, (float)src[d + 1], acc[2 * i + 1]);
-      }
+  for (int i = 0; i < 4; ++i) acc[i] = none ? 0.f : acc[i] * inv;
+  const int64_t at = (int64_t)row * D + d0;
+  if (whole && reinterpret_cast<uintptr_t>(a.o) % 16 == 0) {
+    if (a.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.o) + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    } else {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[0], acc[1]), y = __floats2bfloat162_rn(acc[2], acc[3]);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
     }
+  } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int d = d0 + 64 * (i / 2) + 2 * lane + (i & 1);
-      if (d >= a.D_c) continue;
-      if (a.out_f32) static_cast<float*>(a.o)[(int64_t)row * a.D_c + d] = acc[i];
-      else static_cast<__nv_bfloat16*>(a.o)[(int64_t)row * a.D_c + d] = __float2bfloat16_rn(acc[i]);
+    for (int i = 0; i < 4; ++i) {
+      if (d0 + i >= D) break;
+      if (a.out_f32) static_cast<float*>(a.o)[at + i] = acc[i];
+      else static_cast<__nv_bfloat16*>(a.o)[at + i] = __float2bfloat16_rn(acc[i]);
     }
   }
 }
@@ -228,10 +276,19 @@ cudaError_t launch_verify8_simt(const Verify8Args& a, const VerifyPlan& p, cudaS
 }
 
 cudaError_t launch_combine8(const Verify8Args& a, const VerifyPlan& p, cudaStream_t stream) {
-  const int grid = (p.total_rows + 7) / 8;
-  if (p.part_f16) combine8_kernel<__half><<<grid, 256, 0, stream>>>(a, p);
-  else combine8_kernel<float><<<grid, 256, 0, stream>>>(a, p);
-  return cudaGetLastError();
+  // a programmatic dependent of the attention kernel: its launch overlaps that
+  // kernel's end, its reads wait for it
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.total_rows);
+  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return p.part_f16 ? cudaLaunchKernelEx(&cfg, combine8_kernel<__half>, a, p)
+                    : cudaLaunchKernelEx(&cfg, combine8_kernel<float>, a, p);
 }
 
 }  // namespace kdv

@@ -61,7 +61,8 @@ constexpr int PARTS = 5;                     // blocks of a tile: rope, latent 0
 constexpr int RING = 7;
 constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;
 constexpr int KS_BUFS = 4;
-constexpr int SOFTMAX_WARPS = 8, MMA_WARP = 8, PRODUCER_WARPS = 3;
+constexpr int GROUPS = 4, GROUP_ROWS = ROWS / GROUPS;       // softmax warpgroups, 16 query rows each
+constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 4;
 constexpr int THREADS = (SOFTMAX_WARPS + 1 + PRODUCER_WARPS) * 32;
 constexpr float P_TOP = 12.f, P_GROW = 15.f; // log2 of the largest p when the reference is set / allowed later
 constexpr float UNIT_ROOM = 4.f;             // how far scales may grow before their unit moves
@@ -77,10 +78,10 @@ constexpr int OFF_KS = OFF_RING + RING * BLOCK;            // float [KS_BUFS][12
 constexpr int OFF_OK = OFF_KS + KS_BUFS * KEYS * 4;        // u32 [KS_BUFS][4] readable keys
 constexpr int OFF_MASK = OFF_OK + KS_BUFS * 16;            // u64 [64] node masks by row
 constexpr int OFF_CM = OFF_MASK + ROWS * 8;                // float4 [32]: (c, c', -m, -m') of a row pair
-constexpr int OFF_RED = OFF_CM + 32 * 16;                  // float [2][4][32]
-constexpr int OFF_FAC = OFF_RED + 2 * 4 * 32 * 4;          // float [64] per-row factors
-constexpr int OFF_RED2 = OFF_FAC + ROWS * 4;               // float [2][4]
-constexpr int OFF_BAR = OFF_RED2 + 32;
+constexpr int OFF_RED = OFF_CM + 32 * 16;                  // float [GROUPS][4][16]
+constexpr int OFF_FAC = OFF_RED + GROUPS * 4 * GROUP_ROWS * 4;   // float [64] per-row factors
+constexpr int OFF_RED2 = OFF_FAC + ROWS * 4;               // float [GROUPS][4]
+constexpr int OFF_BAR = OFF_RED2 + GROUPS * 16;
 constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_KS = B_EMPTY + RING, B_S = B_KS + KS_BUFS, B_P = B_S + 2, B_ROPE = B_P + 1,
               B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
 constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
@@ -125,9 +126,28 @@ __device__ __forceinline__ uint64_t global_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// Waits within the CTA. (The cluster-scope forms of the shared header cost this
+// kernel about 500 clocks each.)
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
@@ -138,12 +158,12 @@ struct Waiter {
   int32_t* d_err;
   uint64_t limit;
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try(bar, parity)) return true;
     return slow(bar, parity);
   }
   __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const {
     const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try(bar, parity)) {
       if (*abort) return false;
       if (global_ns() - t0 > limit) {
         *abort = 1;
@@ -245,11 +265,11 @@ struct QueryRow {
   }
 };
 
-// Reduction of 32 values a lane over the warp's lanes: halves of the rows swap
-// sides, so that lane r ends with row r (31 shuffles where a reduction per row takes 32 times five).
-template <typename F> __device__ __forceinline__ float transpose_reduce(float (&v)[32], int lane, F join) {
+// Reduction of 16 values a lane over the warp's lanes: halves of the rows swap
+// sides, so that lane r ends with row r mod 16 (16 shuffles, where a reduction for each row takes 80).
+template <typename F> __device__ __forceinline__ float transpose_reduce(float (&v)[16], int lane, F join) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 8; o > 0; o >>= 1) {
     const bool up = (lane & o) != 0;
 #pragma unroll
     for (int k = 0; k < o; ++k) {
@@ -257,7 +277,21 @@ template <typename F> __device__ __forceinline__ float transpose_reduce(float (&
       v[k] = join(keep, __shfl_xor_sync(0xffffffffu, send, o));
     }
   }
-  return v[0];
+  return join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 // Two fp16 numerators -> their three e5m2 terms: the upper bytes of the first
@@ -295,12 +329,24 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   const int NT = (k_hi - k_lo + KEYS - 1) / KEYS;
   const int r0 = rt * ROWS;
 
+  // this warp's query rows: on their way while the CTA sets up
+  QueryRow row[4];
+  uint64_t qmask[4] = {0, 0, 0, 0};
+  if (warp < SOFTMAX_WARPS) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int lr = r0 + 4 * warp + k;
+      row[k].load(q + ((int64_t)p.tree_base[b] * p.H + lr) * a.q_row_stride, lr < rows_b, lane);
+      if (lane == 0 && lr < rows_b) qmask[k] = node_mask(a, p, b, lr / p.H);
+    }
+  }
   if (tid == 0) {
     for (int i = 0; i < RING; ++i) {
-      mbar_init(bar(B_FULL + i), 1);
+      mbar_init(bar(B_FULL + i), PRODUCER_WARPS);
       mbar_init(bar(B_EMPTY + i), 1);
     }
-    for (int i = 0; i < KS_BUFS; ++i) mbar_init(bar(B_KS + i), 1);
+    for (int i = 0; i < KS_BUFS; ++i) mbar_init(bar(B_KS + i), PRODUCER_WARPS);
     mbar_init(bar(B_S), 1);
     mbar_init(bar(B_S + 1), 1);
     mbar_init(bar(B_P), SOFTMAX_WARPS);
@@ -321,78 +367,90 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 
   if (warp > MMA_WARP) {
     // ---------------------------------------------------------- producers
+    // Each warp brings its 32 keys of every block, so that a block freed by
+    // P.V is full again as soon as may be; up to INFLIGHT blocks in flight.
     const int64_t kv_base = a.kv_off[b];
-    auto load_slots = [&](int tile, int (&slot)[4]) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int j = k_lo + tile * KEYS + g * 32 + lane;
-        slot[g] = -1;
-        if (tile < NT && j < k_hi) {
-          const int64_t s = a.page_table ? (int64_t)a.page_table[kv_base + j] : kv_base + j;
-          if (s >= 0 && s < a.num_slots) slot[g] = (int)s; else slot[g] = -2;
-        }
-      }
+    const int mine = warp - MMA_WARP - 1;            // keys 32 mine .. 32 mine + 31 of a tile
+    auto load_slot = [&](int tile) {                 // of this lane's key; -1 none, -2 outside the pool
+      const int j = k_lo + tile * KEYS + mine * 32 + lane;
+      if (tile >= NT || j >= k_hi) return -1;
+      const int64_t s = a.page_table ? (int64_t)a.page_table[kv_base + j] : kv_base + j;
+      return s >= 0 && s < a.num_slots ? (int)s : -2;
     };
-    int next[4];
-    int n = warp - MMA_WARP - 1, pending = -1;       // pending: the ring place whose rows are in flight
-    auto arrive = [&]() {                            // all but the last group have landed
+    constexpr int INFLIGHT = 3;
+    const int sub = lane >> 3, col = (lane & 7) * 16;
+    uint32_t dst[8];                                 // of this lane's pieces within a block
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dst[q] = base + OFF_RING + swz128((mine * 32 + q * 4 + sub) * 128 + col);
+    int pos = 0, use = 0, first = 0, pending = 0;    // the next place of the ring; oldest place in flight, how many are
+    auto hand_over = [&](int count) {                // the oldest `count` have landed
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_FULL + pending));
+      for (int x = 0; x < count; ++x) {
+        if (lane == 0) mbar_arrive(bar(B_FULL + first));
+        first = first + 1 == RING ? 0 : first + 1;
+      }
+      pending -= count;
     };
-    load_slots(n / PARTS, next);
-    for (; n < NT * PARTS; n += PRODUCER_WARPS) {
-      const int tile = n / PARTS, part = n % PARTS, pos = n % RING, use = n / RING;
-      int slot[4];
+    // The ring holds little more than a tile, so a block's load starts late;
+    // its rows are asked into L2 two tiles before (a lane its key's five lines).
+    auto prefetch = [&](int slot) {
+      if (slot < 0) return;
+      const uint8_t* c = a.c8 + (int64_t)slot * DC;
+      prefetch_l2(a.kr + (int64_t)slot * DR);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) slot[g] = next[g];
-      load_slots((n + PRODUCER_WARPS) / PARTS, next);
-      if (use > 0 && !__all_sync(0xffffffffu, mbar_test_wait(bar(B_EMPTY + pos), (use - 1) & 1))) {
-        if (pending >= 0) {                          // nothing to add yet: hand over what is in flight
-          cp_async_wait<0>();
-          arrive();
-          pending = -1;
+      for (int x = 0; x < 4; ++x) prefetch_l2(c + 128 * x);
+    };
+    int next = load_slot(0), after = load_slot(1);
+    prefetch(after);
+    bool go = true;
+    for (int tile = 0; tile < NT && go; ++tile) {
+      const int slot = next;
+      next = after;
+      after = load_slot(tile + 2);
+      int s[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] = __shfl_sync(0xffffffffu, slot, q * 4 + sub);
+#pragma unroll 1
+      for (int part = 0; part < PARTS; ++part) {
+        if (use > 0 && !__all_sync(0xffffffffu, mbar_test(bar(B_EMPTY + pos), (use - 1) & 1))) {
+          if (pending > 0) {                         // nothing to add yet: hand over what is in flight
+            cp_async_wait<0>();
+            hand_over(pending);
+          }
+          if (!__all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1))) {
+            go = false;
+            break;
+          }
         }
-        if (!__all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1))) break;
-      }
-      const uint32_t dst = base + OFF_RING + pos * BLOCK;
-      const int sub = lane >> 3, col = (lane & 7) * 16;
-      const uint8_t* src0 = part == 0 ? reinterpret_cast<const uint8_t*>(a.kr) + col : a.c8 + (part - 1) * 128 + col;
-      const int64_t pitch = part == 0 ? DR * 2 : DC;
+        const uint8_t* src0 = part == 0 ? reinterpret_cast<const uint8_t*>(a.kr) + col : a.c8 + (part - 1) * 128 + col;
+        const int64_t pitch = part == 0 ? DR * 2 : DC;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        int s[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) s[q] = __shfl_sync(0xffffffffu, slot[g], q * 4 + sub);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const int row = g * 32 + q * 4 + sub;
-          cp_async16(dst + swz128(row * 128 + col), src0 + (s[q] < 0 ? 0 : s[q]) * pitch, s[q] < 0 ? 0 : 16);
+        for (int q = 0; q < 8; ++q) cp_async16(dst[q] + pos * BLOCK, src0 + (s[q] < 0 ? 0 : s[q]) * pitch, s[q] < 0 ? 0 : 16);
+        cp_async_commit();
+        if (part == 0) {
+          const float ks = slot < 0 ? 0.f : a.kv_scale[slot >> a.block_log2];
+          const uint32_t okw = __ballot_sync(0xffffffffu, slot >= 0);
+          reinterpret_cast<float*>(sp + OFF_KS)[(tile % KS_BUFS) * KEYS + mine * 32 + lane] =
+              finite(ks) ? ks : __int_as_float(0x7fc00000);              // a row of infinities has NaN logits
+          if (lane == 0) reinterpret_cast<uint32_t*>(sp + OFF_OK)[(tile % KS_BUFS) * 4 + mine] = okw;
+          if (slot == -2) record_error(a.d_err, KDV_DERR_BAD_SLOT);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_KS + tile % KS_BUFS));
+        }
+        if (part == PARTS - 1) prefetch(after);
+        if (++pending == INFLIGHT) {
+          cp_async_wait<INFLIGHT - 1>();
+          hand_over(1);
+        }
+        if (++pos == RING) {
+          pos = 0;
+          ++use;
         }
       }
-      cp_async_commit();
-      if (part == 0) {
-        float* ks = reinterpret_cast<float*>(sp + OFF_KS) + (tile % KS_BUFS) * KEYS;
-        uint32_t* okw = reinterpret_cast<uint32_t*>(sp + OFF_OK) + (tile % KS_BUFS) * 4;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float s = slot[g] < 0 ? 0.f : a.kv_scale[slot[g] >> a.block_log2];
-          ks[g * 32 + lane] = finite(s) ? s : __int_as_float(0x7fc00000);   // a row of infinities has NaN logits
-          const uint32_t m = __ballot_sync(0xffffffffu, slot[g] >= 0);
-          if (lane == 0) okw[g] = m;
-          if (slot[g] == -2) record_error(a.d_err, KDV_DERR_BAD_SLOT);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_KS + tile % KS_BUFS));
-      }
-      if (pending >= 0) {
-        cp_async_wait<1>();
-        arrive();
-      }
-      pending = pos;
     }
     cp_async_wait<0>();
-    if (pending >= 0) arrive();
+    hand_over(pending);
   } else if (warp == MMA_WARP) {
     // ---------------------------------------------------------- MMA issue
     if (NT > 0) {
@@ -401,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       const uint64_t k_desc = sw128_desc(base + OFF_RING, 16, 1024), v_desc = sw128_desc(base + OFF_RING, BLOCK, 1024);
       auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
       int tile = 0, part = 0, pos = 0, use = 0;      // the next block of Q.K^T
-      auto ready = [&]() { return all(mbar_test_wait(bar(B_FULL + pos), use & 1)); };
+      auto ready = [&]() { return all(mbar_test(bar(B_FULL + pos), use & 1)); };
       // Q.K^T of that block (its barrier has been waited for)
       auto qk = [&]() {
         const uint64_t kb = k_desc + (uint32_t)(pos * (BLOCK / 16));
@@ -443,7 +501,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         if (i >= 0) {
           // the next tile's blocks while this tile's numerators are not ready;
           // the ring holds up to its third
-          while (tile == i + 1 && tile < NT && part < 3 && go && !all(mbar_test_wait(bar(B_P), i & 1))) {
+          while (tile == i + 1 && tile < NT && part < 3 && go && !all(mbar_test(bar(B_P), i & 1))) {
             if (ready()) go = qk();
             else if (all(*abort != 0)) go = false;
           }
@@ -477,52 +535,44 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       if (elect_one()) tc_commit(bar(B_FIN));
       __syncwarp();
       const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(bar(B_FIN), 0) && global_ns() - t0 < TIMEOUT_NS) {}
+      while (!mbar_try(bar(B_FIN), 0) && global_ns() - t0 < TIMEOUT_NS) {}
     }
     __syncwarp();
   } else {
     // ------------------------------------------------- queries and softmax
     const int g = warp >> 2, w = warp & 3;           // warpgroup, lane quarter
-    float4* cm = reinterpret_cast<float4*>(sp + OFF_CM);
-    uint64_t* rmask = reinterpret_cast<uint64_t*>(sp + OFF_MASK);
-    float* fac = reinterpret_cast<float*>(sp + OFF_FAC);
-    float* red = reinterpret_cast<float*>(sp + OFF_RED) + g * 128;
+    float4* cm = reinterpret_cast<float4*>(sp + OFF_CM) + g * (GROUP_ROWS / 2);    // this group's
+    uint64_t* rmask = reinterpret_cast<uint64_t*>(sp + OFF_MASK) + g * GROUP_ROWS;
+    float* fac = reinterpret_cast<float*>(sp + OFF_FAC) + g * GROUP_ROWS;
+    float* red = reinterpret_cast<float*>(sp + OFF_RED) + g * 4 * GROUP_ROWS;
     float* red2 = reinterpret_cast<float*>(sp + OFF_RED2) + g * 4;
     const uint32_t wg_bar = 1 + g;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {                    // four rows' loads in flight
-      QueryRow row[4];
+    {
+      // a warp stages four rows of its group, all loads in flight
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int lr = r0 + warp + SOFTMAX_WARPS * (4 * h + k);
-        row[k].load(q + ((int64_t)p.tree_base[b] * p.H + lr) * a.q_row_stride, lr < rows_b, lane);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = warp + SOFTMAX_WARPS * (4 * h + k), lr = r0 + r;
+        const int r = 4 * warp + k;
         const float c = row[k].stage(a.scale, r, sp, lane);
         if (lane == 0) {
-          float* f = reinterpret_cast<float*>(cm + r / 2) + (r & 1);
+          float* f = reinterpret_cast<float*>(sp + OFF_CM) + (r / 2) * 4 + (r & 1);
           f[0] = c;
           f[2] = -NO_MAX;
-          rmask[r] = lr < rows_b ? node_mask(a, p, b, lr / p.H) : 0ull;
+          reinterpret_cast<uint64_t*>(sp + OFF_MASK)[r] = qmask[k];
         }
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(B_Q));
-    named_bar_sync(3, SOFTMAX_WARPS * 32);           // both groups have written cm and rmask
+    named_bar_sync(wg_bar, 128);                     // the group's cm and rmask are written
 
-    float l[32];
+    float l[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) l[i] = 0.f;
+    for (int i = 0; i < 16; ++i) l[i] = 0.f;
     float unit = 0.f, inv_unit = 0.f;                // the power of two that s_j is taken relative to
-    const uint32_t quarter = (uint32_t)(w * 32) << 16;
+    const uint32_t quarter = tmem + ((uint32_t)(w * 32) << 16);
     const int key = w * 32 + lane;
-    uint8_t* prow = sp + OFF_P + key * ROWS;
-    const uint32_t psw = ((uint32_t)key >> 1) & 3u;  // 64-byte swizzle of this key's row
+    uint8_t* prow = sp + OFF_P + key * ROWS + (((uint32_t)g ^ (((uint32_t)key >> 1) & 3u)) << 4);   // 64-byte swizzle
 
     for (int i = 0; i < NT; ++i) {
       wait(bar(B_KS + i % KS_BUFS), (i / KS_BUFS) & 1);
@@ -533,17 +583,17 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       const bool plain = __all_sync(0xffffffffu, readable && u < 0);
       wait(bar(B_S + (i & 1)), (i >> 1) & 1);
       tc_fence_after();
-      float t[32];
+      float t[16];
       bool dirty;
       auto scores = [&]() {                          // t = s_j (q . k), -inf where the row does not see the key
-        uint32_t hi[32], lo[32];
-        const uint32_t sb = tmem + quarter + TM_S + (i & 1) * 128 + 32 * g;
-        tmem_ld32(sb, hi);
-        tmem_ld32(sb + 64, lo);
+        uint32_t hi[16], lo[16];
+        const uint32_t sb = quarter + TM_S + (i & 1) * 128 + GROUP_ROWS * g;
+        tmem_ld16(sb, hi);
+        tmem_ld16(sb + 64, lo);
         tmem_wait_ld();
         dirty = isnan(__uint_as_float(lo[0]));
 #pragma unroll
-        for (int r = 0; r < 32; r += 2) {
+        for (int r = 0; r < 16; r += 2) {
           float2 x = fma_f32x2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), make_float2(0.0625f, 0.0625f),
                                make_float2(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
           x = mul_f32x2(x, make_float2(s, s));
@@ -552,8 +602,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         }
         if (!plain) {
 #pragma unroll
-          for (int r = 0; r < 32; ++r) {
-            const bool vis = readable && (u < 0 || ((rmask[32 * g + r] >> u) & 1ull));
+          for (int r = 0; r < 16; ++r) {
+            const bool vis = readable && (u < 0 || ((rmask[r] >> u) & 1ull));
             t[r] = vis ? t[r] : -INFINITY;
           }
         }
@@ -561,8 +611,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       auto exponents = [&]() {                       // t = log2 of the numerators; the largest
         float top = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < 32; r += 2) {
-          const float4 f = cm[16 * g + r / 2];
+        for (int r = 0; r < 16; r += 2) {
+          const float4 f = cm[r / 2];
           const float2 d = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
           t[r] = d.x;
           t[r + 1] = d.y;
@@ -581,23 +631,26 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
         }
       }
-      const bool move = exponents() > P_GROW || fabsf(s) > unit;
-      if (named_bar_or(wg_bar, 128, move)) {
+      // the first tile sets the reference in any case
+      const bool move = i == 0 || exponents() > P_GROW || fabsf(s) > unit;
+      if (i == 0 || named_bar_or(wg_bar, 128, move)) {
         // ---- some reference moves: maxima over the tile's keys, per row
-        scores();
+        if (i > 0) scores();
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          const float4 f = cm[16 * g + r / 2];
-          t[r] *= (r & 1) ? f.y : f.x;
+        for (int r = 0; r < 16; r += 2) {
+          const float4 f = cm[r / 2];
+          t[r] *= f.x;
+          t[r + 1] *= f.y;
         }
         const float mine = transpose_reduce(t, lane, [](float x, float y) { return fmaxf(x, y); });   // of row `lane`
-        red[w * 32 + lane] = mine;
+        if (lane < GROUP_ROWS) red[w * GROUP_ROWS + lane] = mine;
         const float smax = warp_max(isnan(s) ? 0.f : fabsf(s));
         if (lane == 0) red2[w] = smax;
         named_bar_sync(wg_bar, 128);
-        const float top = fmaxf(fmaxf(red[lane], red[32 + lane]), fmaxf(red[64 + lane], red[96 + lane]));   // NaN: no key moves it
+        const int row = lane & (GROUP_ROWS - 1);
+        const float top = fmaxf(fmaxf(red[row], red[16 + row]), fmaxf(red[32 + row], red[48 + row]));   // NaN: no key moves it
         const float st = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
-        float* cr = reinterpret_cast<float*>(cm + 16 * g + lane / 2) + (lane & 1);
+        float* cr = reinterpret_cast<float*>(cm + row / 2) + (row & 1);
         const float m_old = -cr[2];
         const float m_new = top - P_TOP > m_old ? top - P_TOP : m_old;
         float unit_new = unit;
@@ -610,26 +663,26 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         }
         const float shift = ex2(m_old - m_new);
         named_bar_sync(wg_bar, 128);                 // all have read red, red2 and cm
-        if (w == 0) {
+        if (w == 0 && lane < GROUP_ROWS) {
           cr[2] = -m_new;
-          fac[32 * g + lane] = shift;
+          fac[lane] = shift;
         }
         named_bar_sync(wg_bar, 128);
         const float us = unit / unit_new;
         unit = unit_new;
         inv_unit = 1.f / unit_new;
-#pragma unroll
-        for (int r = 0; r < 32; ++r) l[r] *= fac[32 * g + r];
         if (i > 0) {
           // P.V of the tiles before is complete: this tile's S was committed behind it
+#pragma unroll
+          for (int r = 0; r < 16; ++r) l[r] *= fac[r];
 #pragma unroll 1
           for (int mt = 0; mt < 4; ++mt) {
-            uint32_t o[32];
-            tmem_ld32(tmem + quarter + mt * 64 + 32 * g, o);
+            uint32_t o[16];
+            tmem_ld16(quarter + mt * 64 + GROUP_ROWS * g, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 32; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * (fac[32 * g + r] * us));
-            tmem_st32(tmem + quarter + mt * 64 + 32 * g, o);
+            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * (fac[r] * us));
+            tmem_st16(quarter + mt * 64 + GROUP_ROWS * g, o);
           }
           tmem_wait_st();
         }
@@ -637,59 +690,56 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         exponents();
       }
       const float sr = s * inv_unit;
+      uint32_t w0[4], w1[4], w2[4];                  // 16 rows = 16 bytes of each term
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {                  // 16 rows = 16 bytes of each term
-        uint32_t w0[4], w1[4], w2[4];
+      for (int q4 = 0; q4 < 4; ++q4) {
+        uint32_t t0[2], t1[2], t2[2];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          uint32_t t0[2], t1[2], t2[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int r = 16 * h + 4 * q4 + 2 * k;
-            const float p0 = ex2(t[r]), p1 = ex2(t[r + 1]);
-            const float2 sum = add_f32x2(make_float2(l[r], l[r + 1]), make_float2(p0, p1));
-            l[r] = sum.x;
-            l[r + 1] = sum.y;
-            float2 e = mul_f32x2(make_float2(p0, p1), make_float2(sr, sr));
-            if (!plain) {                            // an unseen key's scale may be NaN
-              e.x = p0 == 0.f ? 0.f : e.x;
-              e.y = p1 == 0.f ? 0.f : e.y;
-            }
-            split_p(pack_f16x2(e.x, e.y), t0[k], t1[k], t2[k]);
+        for (int k = 0; k < 2; ++k) {
+          const int r = 4 * q4 + 2 * k;
+          const float p0 = ex2(t[r]), p1 = ex2(t[r + 1]);
+          const float2 sum = add_f32x2(make_float2(l[r], l[r + 1]), make_float2(p0, p1));
+          l[r] = sum.x;
+          l[r + 1] = sum.y;
+          float2 e = mul_f32x2(make_float2(p0, p1), make_float2(sr, sr));
+          if (!plain) {                              // an unseen key's scale may be NaN
+            e.x = p0 == 0.f ? 0.f : e.x;
+            e.y = p1 == 0.f ? 0.f : e.y;
           }
-          w0[q4] = __byte_perm(t0[0], t0[1], 0x7531);
-          w1[q4] = __byte_perm(t1[0], t1[1], 0x7531);
-          w2[q4] = t2[0] | (t2[1] << 16);
+          split_p(pack_f16x2(e.x, e.y), t0[k], t1[k], t2[k]);
         }
-        uint8_t* at = prow + ((((uint32_t)(2 * g + h)) ^ psw) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-        *reinterpret_cast<uint4*>(at + P_BYTES) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-        *reinterpret_cast<uint4*>(at + 2 * P_BYTES) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        w0[q4] = __byte_perm(t0[0], t0[1], 0x7531);
+        w1[q4] = __byte_perm(t1[0], t1[1], 0x7531);
+        w2[q4] = t2[0] | (t2[1] << 16);
       }
+      *reinterpret_cast<uint4*>(prow) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+      *reinterpret_cast<uint4*>(prow + P_BYTES) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+      *reinterpret_cast<uint4*>(prow + 2 * P_BYTES) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_P));
     }
 
+    if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");   // the merge's launch overlaps the rest
     // ---- row sums over the 128 lanes
-    transpose_reduce(l, lane, [](float x, float y) { return x + y; });
+    const float part = transpose_reduce(l, lane, [](float x, float y) { return x + y; });
     named_bar_sync(wg_bar, 128);
-    red[w * 32 + lane] = l[0];
+    if (lane < GROUP_ROWS) red[w * GROUP_ROWS + lane] = part;
     named_bar_sync(wg_bar, 128);
-    const float sum = (red[lane] + red[32 + lane]) + (red[64 + lane] + red[96 + lane]);
-    const float m = -(reinterpret_cast<const float*>(cm + 16 * g + lane / 2) + (lane & 1))[2];
-    const bool none = sum == 0.f;
-    const float inv = none ? 0.f : 1.f / sum;
-    const float lse = none ? -INFINITY : LN2 * (m + log2f(sum));
     const bool direct = p.out_mode == OUT_DIRECT;
-    if (w == 0) {
-      const int lr = r0 + 32 * g + lane;
-      fac[32 * g + lane] = direct ? inv * unit : inv;
-      if (lr < rows_b) {
-        const int64_t orow = out_row_index(p, b, split, lr);
-        if (!direct) a.part_s[orow] = make_float2(lse, unit);
-        else if (a.lse != nullptr) a.lse[orow] = lse;
+    const int64_t orow0 = out_row_index(p, b, split, r0 + GROUP_ROWS * g);
+    const int nr = min(GROUP_ROWS, rows_b - r0 - GROUP_ROWS * g);      // rows to write, may be below 0
+    if (w == 0 && lane < GROUP_ROWS) {
+      const float sum = (red[lane] + red[16 + lane]) + (red[32 + lane] + red[48 + lane]);
+      const float m = -(reinterpret_cast<const float*>(cm + lane / 2) + (lane & 1))[2];
+      const bool none = sum == 0.f;
+      const float inv = none ? 0.f : 1.f / sum;
+      const float lse = none ? -INFINITY : LN2 * (m + log2f(sum));
+      fac[lane] = direct ? inv * unit : inv;
+      if (lane < nr) {
+        if (!direct) a.part_s[orow0 + lane] = make_float2(lse, unit);
+        else if (a.lse != nullptr) a.lse[orow0 + lane] = lse;
       }
     }
     named_bar_sync(wg_bar, 128);
@@ -697,38 +747,38 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     tc_fence_after();
     // Output: lanes are dims and columns rows, so a block of 128 dims goes
     // through shared memory (the ring is free) and leaves in 16-byte pieces of rows.
-    const int64_t orow0 = out_row_index(p, b, split, r0 + 32 * g);
-    const int nr = min(32, rows_b - r0 - 32 * g);
-    const bool wide = direct && a.out_f32;
-    const uint32_t line = wide ? 512 : 256;          // bytes of a row's 128 dims
-    uint8_t* out = static_cast<uint8_t*>(direct ? a.o : a.part_o);
-#pragma unroll 1
-    for (int mt = 0; mt < 4; ++mt) {
-      uint8_t* stage = sp + OFF_RING + (2 * g + (mt & 1)) * BLOCK;
-      uint32_t o[32];
-      if (NT > 0) {
-        tmem_ld32(tmem + quarter + mt * 64 + 32 * g, o);
-        tmem_wait_ld();
-      } else {
+    uint8_t* stage = sp + OFF_RING + g * (2 * GROUP_ROWS * 512);
+    auto write = [&](auto zero, auto convert, void* dst) {
+      using T = decltype(zero);
+      constexpr int LINE = 128 * sizeof(T), PER = LINE / 16;
+      uint8_t* out = static_cast<uint8_t*>(dst) + orow0 * 4 * LINE;
 #pragma unroll
-        for (int r = 0; r < 32; ++r) o[r] = 0u;
-      }
+      for (int mt = 0; mt < 4; ++mt) {
+        T* buf = reinterpret_cast<T*>(stage + (mt & 1) * (GROUP_ROWS * 512));
+        uint32_t o[16];
+        if (NT > 0) {
+          tmem_ld16(quarter + mt * 64 + GROUP_ROWS * g, o);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        const float f = fac[32 * g + r];
-        const float v = f == 0.f ? 0.f : __uint_as_float(o[r]) * f;
-        uint8_t* at = stage + r * line;
-        if (wide) reinterpret_cast<float*>(at)[key] = v;
-        else if (direct) reinterpret_cast<__nv_bfloat16*>(at)[key] = __float2bfloat16_rn(v);
-        else reinterpret_cast<__half*>(at)[key] = __float2half_rn(v);
+          for (int r = 0; r < 16; ++r) o[r] = 0u;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float f = fac[r];
+          buf[r * 128 + key] = convert(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
+        }
+        named_bar_sync(wg_bar, 128);                 // the other buffer's readers have passed the barrier before this one
+#pragma unroll
+        for (int x = key; x < GROUP_ROWS * PER; x += 128) {
+          const int r = x / PER, c = x % PER;
+          if (r < nr) reinterpret_cast<uint4*>(out + (r * 4 + mt) * LINE)[c] = reinterpret_cast<const uint4*>(buf + r * 128)[c];
+        }
       }
-      named_bar_sync(wg_bar, 128);                   // the other buffer's readers have passed the barrier before this one
-      const int per = (int)line / 16;
-      for (int x = key; x < nr * per; x += 128) {
-        const int r = x / per, c = (x - r * per) * 16;
-        *reinterpret_cast<uint4*>(out + ((orow0 + r) * 4 + mt) * line + c) = *reinterpret_cast<const uint4*>(stage + r * line + c);
-      }
-    }
+    };
+    if (!direct) write(__half(), [](float v) { return __float2half_rn(v); }, a.part_o);
+    else if (a.out_f32) write(float(), [](float v) { return v; }, a.o);
+    else write(__nv_bfloat16(), [](float v) { return __float2bfloat16_rn(v); }, a.o);
     tc_fence_before();
   }
   __syncthreads();
