@@ -5,14 +5,17 @@
 //   + bias; -inf where the grammar forbids it. made counts the request's own
 //   output tokens in its history plus the drafted tokens on the node's path.
 //
-// Bound: HBM (every logit read and written once, 1/8 byte of grammar mask).
-// One CTA takes a tile of the vocabulary for all nodes of one request: it
-// counts the request's history into a table of the tile's tokens in shared
-// memory once (the history is read from L2 by every tile's CTA; a table of
-// counts in memory would be 4 bytes a token a request, twice a bf16 row), adds
-// the biases, and then streams each node's logits through registers. A node's
-// path holds at most 64 tokens: where some of them fall into the tile, their
-// counts are added for that node and taken away again after it.
+// Bound: HBM (every logit read and written once, 1/8 byte of grammar mask);
+// for one request's tree the fixed part: launch, and the history's way from L2.
+// One CTA takes a tile of the vocabulary for some nodes of one request. It counts the
+// request's history into a table of the tile's tokens in shared memory (the
+// history is read from L2 by every tile's CTA; a table of counts in memory would be 4 bytes a token
+// a request, twice a bf16 row). A thread then notes whether any of its eight tokens has a count or a
+// bias at all and streams the logits, two nodes in flight, the first two asked for before the history is read. Drafted tokens are not counted into the table:
+// each one in the tile has a number there, and a small matrix says how often
+// node t's path holds it, so the nodes need no barrier between them.
+// 13 nodes of 163840 tokens with 5553 of history: 10 us (38 with the tile's nodes one after
+// another and the path counted in and out around each); 160 nodes in fp32: 67 us (87).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -23,6 +26,9 @@ namespace kdv {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int TOKENS = 8;                  // tokens a thread holds
+constexpr int TILE = THREADS * TOKENS;     // tokens a CTA holds
+constexpr int NODES = 2;                   // nodes in flight
 
 struct LogitsArgs {
   const void* x;
@@ -45,13 +51,15 @@ struct LogitsArgs {
   int64_t allow_ld;
   const int32_t* allow_row;
   int32_t* d_err;
-  int32_t allow_rows, max_T, total_nodes, vocab, tile;
+  int32_t allow_rows, max_T, total_nodes, vocab;
+  int32_t chunk;           // nodes of one CTA
 };
 
-// count word: 2 * made + (1 if the prompt holds the token)
-__device__ __forceinline__ float process(float x, uint32_t word, float bias, float rep, float pres, float freq) {
+// word: 2 * made + (1 if the prompt holds the token)
+__device__ __forceinline__ float process(float x, uint32_t word, float bias, float rep, float inv, bool normal, float pres, float freq) {
   if (word != 0u) {
-    x = x > 0.f ? x / rep : x * rep;
+    const float low = normal ? x * inv : x / rep;
+    x = x > 0.f ? low : x * rep;
     const uint32_t made = word >> 1;
     x -= freq * (float)made;
     if (made != 0u) x -= pres;
@@ -59,87 +67,155 @@ __device__ __forceinline__ float process(float x, uint32_t word, float bias, flo
   return x + bias;
 }
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// A thread's eight logits of a node: neighbours in 16-byte pieces (VEC), or 256 apart.
+template <typename T, bool VEC> struct Row;
+template <> struct Row<__nv_bfloat16, true> {
+  uint4 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w = *reinterpret_cast<const uint4*>(p + TOKENS * threadIdx.x); }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t u = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+    return __uint_as_float(j % 2 ? u & 0xffff0000u : u << 16);
   }
+};
+template <> struct Row<float, true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, int) {
+    a = reinterpret_cast<const float4*>(p + TOKENS * threadIdx.x)[0];
+    b = reinterpret_cast<const float4*>(p + TOKENS * threadIdx.x)[1];
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
+  }
+};
+template <typename T> struct Row<T, false> {
+  T v[TOKENS];
+  __device__ __forceinline__ void load(const T* p, int n) {
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j)
+      if ((int)threadIdx.x + j * THREADS < n) v[j] = p[threadIdx.x + j * THREADS];
+  }
+  __device__ __forceinline__ float get(int j) const { return (float)v[j]; }
+};
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-template <typename T> __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      u[i] = *reinterpret_cast<uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// grid (tiles, batch). VEC: rows of both sides 16-byte aligned.
+// grid (tiles, batch, chunks of nodes). VEC: rows of both sides 16-byte
+// aligned and the tile whole; the launch's other tiles (the last one) take the scalar form.
 template <typename TX, typename TY, bool VEC>
-__global__ void __launch_bounds__(THREADS) logits_process_kernel(const __grid_constant__ LogitsArgs a) {
-  extern __shared__ __align__(16) uint32_t smem[];
-  uint32_t* count = smem;                                   // [tile]
-  float* bias = reinterpret_cast<float*>(smem + a.tile);    // [tile]
-  __shared__ int par[KDV_MAX_TREE], tok[KDV_MAX_TREE];
-  const int b = blockIdx.y, v0 = blockIdx.x * a.tile, n = min(a.tile, a.vocab - v0);
-  const bool first = blockIdx.x == 0 && threadIdx.x == 0;   // reports what every tile sees
+__device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* count, float* bias, uint8_t* number,
+                                             uint8_t (*times)[KDV_MAX_TREE], int* par, int* tok) {
+  const int tid = threadIdx.x, b = blockIdx.y, v0 = blockIdx.x * TILE, n = min(TILE, a.vocab - v0);
+  const bool reports = blockIdx.x == 0 && blockIdx.z == 0;  // what every CTA of the request sees
+  // the request's scalars, all asked for at once
   const int t0 = a.tree_off[b], T = a.tree_off[b + 1] - t0;
-  if (T < 0 || T > a.max_T || t0 < 0 || t0 > a.total_nodes - T) {
-    if (first) record_error(a.d_err, KDV_DERR_BAD_LENGTH);
-    return;
-  }
-  if (T == 0) return;
-  for (int i = threadIdx.x; i < a.tile; i += THREADS) {
-    count[i] = 0u;
-    bias[i] = 0.f;
-  }
+  int len = a.hist ? a.hist_len[b] : 0;
+  const int pl = a.hist && a.prompt_len ? a.prompt_len[b] : 0;
+  const int bias_lo = a.bias_off ? a.bias_off[b] : 0, bias_hi = a.bias_off ? a.bias_off[b + 1] : 0;
   float rep = a.repetition ? a.repetition[b] : 1.f;
   const float pres = a.presence ? a.presence[b] : 0.f, freq = a.frequency ? a.frequency[b] : 0.f;
+  if (T < 0 || T > a.max_T || t0 < 0 || t0 > a.total_nodes - T) {
+    if (reports && tid == 0) record_error(a.d_err, KDV_DERR_BAD_LENGTH);
+    return;
+  }
+  const int first = blockIdx.z * a.chunk, last = min(T, first + a.chunk);
+  if (first >= last) return;
+  const TX* x = static_cast<const TX*>(a.x) + (int64_t)t0 * a.x_ld + v0;
+  TY* y = static_cast<TY*>(a.y) + (int64_t)t0 * a.y_ld + v0;
+  // grammar row of node t (null: unconstrained)
+  auto allowed = [&](int t) -> const uint32_t* {
+    if (a.allow == nullptr) return nullptr;
+    const int row = a.allow_row ? a.allow_row[t0 + t] : t0 + t;
+    if (row >= a.allow_rows) {
+      if (blockIdx.x == 0 && tid == 0) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
+      return nullptr;
+    }
+    return row < 0 ? nullptr : a.allow + (int64_t)row * a.allow_ld + v0 / 32;
+  };
+  auto bits_of = [&](const uint32_t* row) -> uint32_t {     // bit j: this thread's token j
+    if (row == nullptr) return 0xffu;
+    if (VEC) return reinterpret_cast<const uint8_t*>(row)[tid];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) {
+      const int i = tid + j * THREADS;
+      if (i < n) bits |= ((row[i / 32] >> (i % 32)) & 1u) << j;
+    }
+    return bits;
+  };
+  int node_parent = -1, node_token = 0;
+  if (a.parent != nullptr && tid < T) {
+    node_parent = a.parent[t0 + tid];
+    node_token = a.token[t0 + tid];
+  }
+  Row<TX, VEC> r[NODES];
+  uint32_t bits[NODES];
+  auto load = [&](int t) {
+#pragma unroll
+    for (int k = 0; k < NODES; ++k)
+      if (t + k < last) {
+        r[k].load(x + (int64_t)(t + k) * a.x_ld, n);
+        bits[k] = bits_of(allowed(t + k));
+      }
+  };
+  load(first);
+
+  for (int i = tid; i < TILE / 4; i += THREADS) {
+    reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint4*>(bias)[i] = make_uint4(0, 0, 0, 0);
+    reinterpret_cast<uint32_t*>(number)[i] = 0u;
+  }
   if (!(rep > 0.f) || !(rep <= 3.402823466e38f)) {
-    if (first) record_error(a.d_err, KDV_DERR_BAD_SCORE);
+    if (reports && tid == 0) record_error(a.d_err, KDV_DERR_BAD_SCORE);
     rep = 1.f;
   }
   // the tree's path data
-  const bool paths = a.parent != nullptr;
-  if (threadIdx.x < T && paths) {
-    const int u = threadIdx.x, p = a.parent[t0 + u], k = a.token[t0 + u];
-    const bool bad = p < -1 || p >= u;
+  bool bad = false, mine = false;
+  if (a.parent != nullptr && tid < T) {
+    const int p = node_parent, k = node_token;
+    bad = p < -1 || p >= tid;
     const bool bad_tok = p >= 0 && (k < 0 || k >= a.vocab);
-    if (blockIdx.x == 0 && (bad || bad_tok)) record_error(a.d_err, bad ? KDV_DERR_BAD_PARENT : KDV_DERR_BAD_TOKEN);
-    par[u] = p;
-    tok[u] = (p < 0 || bad_tok) ? -1 : k;                   // roots are in the history already
+    if (reports && (bad || bad_tok)) record_error(a.d_err, bad ? KDV_DERR_BAD_PARENT : KDV_DERR_BAD_TOKEN);
+    par[tid] = p;
+    mine = p >= 0 && k >= v0 && k - v0 < n;                 // roots are in the history already
+    tok[tid] = mine ? k - v0 : -1;
   }
-  const bool tree_ok = !__syncthreads_or(threadIdx.x < T && paths && (par[threadIdx.x] < -1 || par[threadIdx.x] >= (int)threadIdx.x));
+  const bool tree_ok = !__syncthreads_or(bad);
+  const bool drafted = __syncthreads_or(mine) && tree_ok;   // else no node of this tile needs its path
+  if (drafted) {
+    if (mine) {                                             // the token's number: 1 + its first node
+      int w = 0;
+      while (tok[w] != tok[tid]) ++w;
+      number[tok[tid]] = (uint8_t)(w + 1);
+    }
+    for (int i = tid; i < T * T; i += THREADS) times[i / T][i % T] = 0;
+  }
   // history: made tokens add 2, prompt tokens set bit 0
   if (a.hist != nullptr) {
-    int len = a.hist_len[b], pl = a.prompt_len ? a.prompt_len[b] : 0;
     if (len < 0 || len > a.hist_ld || pl < 0) {
-      if (first) record_error(a.d_err, KDV_DERR_BAD_LENGTH);
+      if (reports && tid == 0) record_error(a.d_err, KDV_DERR_BAD_LENGTH);
       len = (int)min((int64_t)max(len, 0), a.hist_ld);
     }
     const int32_t* h = a.hist + b * a.hist_ld;
-    for (int base = threadIdx.x; base < len; base += THREADS * 4) {
-      int k[4];
+    constexpr int FLIGHT = 8;
+    for (int64_t base = tid; base < len; base += THREADS * FLIGHT) {
+      int k[FLIGHT];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = base + j * THREADS < len ? h[base + j * THREADS] : v0 - 1;
+      for (int j = 0; j < FLIGHT; ++j) k[j] = base + j * THREADS < len ? h[base + j * THREADS] : v0 - 1;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = base + j * THREADS;
-        if (i < len && blockIdx.x == 0 && (k[j] < 0 || k[j] >= a.vocab)) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
+      for (int j = 0; j < FLIGHT; ++j) {
+        const int64_t i = base + j * THREADS;
+        if (reports && i < len && (k[j] < 0 || k[j] >= a.vocab)) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
         const uint32_t at = (uint32_t)k[j] - (uint32_t)v0;
         if (i < len && at < (uint32_t)n) {
           if (i < pl) atomicOr(&count[at], 1u); else atomicAdd(&count[at], 2u);
@@ -149,80 +225,121 @@ __global__ void __launch_bounds__(THREADS) logits_process_kernel(const __grid_co
   }
   // biases: ascending tokens, so the tile's entries are one range
   if (a.bias_off != nullptr) {
-    const int lo = a.bias_off[b], hi = a.bias_off[b + 1];
+    const int lo = bias_lo, hi = bias_hi;
     int s = lo, e = hi;
-    while (s < e) {                                         // first entry with token >= v0
+    // first entry with token >= v0; a short list is read through instead (the search's steps wait for one another)
+    while (hi - lo > 16 * THREADS && s < e) {
       const int mid = s + (e - s) / 2;
       if (a.bias_token[mid] < v0) s = mid + 1; else e = mid;
     }
-    for (int i = s + threadIdx.x; i < hi; i += THREADS) {
+    for (int i = s + tid; i < hi; i += THREADS) {
       const int k = a.bias_token[i];
       if (k >= v0 + n) break;
       if (k >= v0 && (i == lo || a.bias_token[i - 1] < k)) bias[k - v0] = a.bias_value[i];
     }
-    if (blockIdx.x == 0)
-      for (int i = lo + threadIdx.x; i < hi; i += THREADS) {
+    if (reports)
+      for (int i = lo + tid; i < hi; i += THREADS) {
         const int k = a.bias_token[i];
         if (k < 0 || k >= a.vocab || (i > lo && a.bias_token[i - 1] >= k)) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
       }
   }
   __syncthreads();
-  // does any drafted token fall into the tile? (else no node needs its path)
-  const bool mine = paths && tree_ok && threadIdx.x < T && (uint32_t)tok[threadIdx.x] - (uint32_t)v0 < (uint32_t)n &&
-                    tok[threadIdx.x] >= 0;
-  const bool drafted = __syncthreads_or(mine);
+  if (drafted) {
+    if (tid < T)
+      for (int u = tid; u >= 0; u = par[u])
+        if (tok[u] >= 0) ++times[tid][number[tok[u]] - 1];
+    __syncthreads();
+  }
 
-  const TX* x = static_cast<const TX*>(a.x);
-  TY* y = static_cast<TY*>(a.y);
-  for (int t = 0; t < T; ++t) {
-    const int node = t0 + t;
-    if (drafted) {
-      __syncthreads();
-      if (threadIdx.x == 0)
-        for (int u = t; u >= 0; u = par[u])
-          if (tok[u] >= v0 && tok[u] - v0 < n) count[tok[u] - v0] += 2u;
-      __syncthreads();
-    }
-    int arow = a.allow_row ? a.allow_row[node] : node;
-    if (a.allow != nullptr && arow >= a.allow_rows) {
-      if (first) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
-      arow = -1;
-    }
-    const uint32_t* allow = a.allow != nullptr && arow >= 0 ? a.allow + (int64_t)arow * a.allow_ld + v0 / 32 : nullptr;
-    const TX* xr = x + (int64_t)node * a.x_ld + v0;
-    TY* yr = y + (int64_t)node * a.y_ld + v0;
-    const int nv = VEC ? n / 8 * 8 : 0;
-    for (int i = threadIdx.x * 8; i < nv; i += THREADS * 8) {
-      float f[8];
-      load8(xr + i, f);
-      const uint32_t bits = allow ? allow[i / 32] >> (i % 32) : 0xffffffffu;
+  auto at = [&](int j) { return VEC ? TOKENS * tid + j : tid + j * THREADS; };
+  uint32_t touched = 0;                                     // not 0: some of this thread's tokens have a count or a bias
+  if (VEC) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        f[j] = process(f[j], count[i + j], bias[i + j], rep, pres, freq);
-        if (!((bits >> j) & 1u)) f[j] = __int_as_float(0xff800000);
+    for (int q = 0; q < 2; ++q) {
+      const uint4 x = reinterpret_cast<const uint4*>(count)[2 * tid + q], z = reinterpret_cast<const uint4*>(bias)[2 * tid + q];
+      touched |= x.x | x.y | x.z | x.w | z.x | z.y | z.z | z.w;
+      if (drafted) touched |= reinterpret_cast<const uint32_t*>(number)[2 * tid + q];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < TOKENS; ++j) touched |= count[at(j)] | __float_as_uint(bias[at(j)]) | number[at(j)];
+  }
+  // x / rep as a product where 1 / rep is a normal number (an fp32 rounding more)
+  const float inv = 1.f / rep;
+  const bool normal = inv >= 1.17549435e-38f && inv <= 3.402823466e38f;
+  for (int t = first; t < last; t += NODES) {
+    if (t > first) load(t);
+    float f[NODES][TOKENS];
+#pragma unroll
+    for (int k = 0; k < NODES; ++k)
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j) f[k][j] = r[k].get(j);
+    if (touched != 0) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {                         // four tokens at a time
+        uint32_t w[4], id[4] = {0, 0, 0, 0};
+        float add[4];
+        if (VEC) {
+          const uint4 x = reinterpret_cast<const uint4*>(count)[2 * tid + q];
+          const float4 z = reinterpret_cast<const float4*>(bias)[2 * tid + q];
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          add[0] = z.x; add[1] = z.y; add[2] = z.z; add[3] = z.w;
+          if (drafted) {
+            const uint32_t u = reinterpret_cast<const uint32_t*>(number)[2 * tid + q];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) id[j] = (u >> (8 * j)) & 0xffu;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = count[at(4 * q + j)];
+            add[j] = bias[at(4 * q + j)];
+            if (drafted) id[j] = number[at(4 * q + j)];
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < NODES; ++k) {
+          if (t + k >= last) break;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t word = id[j] != 0 ? w[j] + 2u * times[t + k][id[j] - 1] : w[j];
+            f[k][4 * q + j] = process(f[k][4 * q + j], word, add[j], rep, inv, normal, pres, freq);
+          }
+        }
       }
-      store8(yr + i, f);
     }
-    for (int i = nv + threadIdx.x; i < n; i += THREADS) {
-      float f = process((float)xr[i], count[i], bias[i], rep, pres, freq);
-      if (allow && !((allow[i / 32] >> (i % 32)) & 1u)) f = __int_as_float(0xff800000);
-      yr[i] = (TY)f;
-    }
-    if (drafted) {
-      __syncthreads();
-      if (threadIdx.x == 0)
-        for (int u = t; u >= 0; u = par[u])
-          if (tok[u] >= v0 && tok[u] - v0 < n) count[tok[u] - v0] -= 2u;
+#pragma unroll
+    for (int k = 0; k < NODES; ++k) {
+      if (t + k >= last) break;
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j)
+        if (!((bits[k] >> j) & 1u)) f[k][j] = __int_as_float(0xff800000);
+      TY* row = y + (int64_t)(t + k) * a.y_ld;
+      if (VEC) {
+        store8(row + TOKENS * tid, f[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < TOKENS; ++j)
+          if (at(j) < n) row[at(j)] = (TY)f[k][j];
+      }
     }
   }
 }
 
 template <typename TX, typename TY>
+__global__ void __launch_bounds__(THREADS, 4) logits_process_kernel(const __grid_constant__ LogitsArgs a, int vec) {
+  __shared__ __align__(16) uint32_t count[TILE];
+  __shared__ __align__(16) float bias[TILE];
+  __shared__ __align__(16) uint8_t number[TILE], times[KDV_MAX_TREE][KDV_MAX_TREE];
+  __shared__ int par[KDV_MAX_TREE], tok[KDV_MAX_TREE];
+  if (vec && (int)(blockIdx.x + 1) * TILE <= a.vocab) process_tile<TX, TY, true>(a, count, bias, number, times, par, tok);
+  else process_tile<TX, TY, false>(a, count, bias, number, times, par, tok);
+}
+
+template <typename TX, typename TY>
 cudaError_t launch_logits(const LogitsArgs& a, int batch, bool vec, cudaStream_t s) {
-  const size_t smem = (size_t)a.tile * 8;
-  const dim3 grid((unsigned)((a.vocab + a.tile - 1) / a.tile), (unsigned)batch);
-  auto k = vec ? logits_process_kernel<TX, TY, true> : logits_process_kernel<TX, TY, false>;
-  k<<<grid, THREADS, smem, s>>>(a);
+  const dim3 grid((unsigned)((a.vocab + TILE - 1) / TILE), (unsigned)batch, (unsigned)((a.max_T + a.chunk - 1) / a.chunk));
+  logits_process_kernel<TX, TY><<<grid, THREADS, 0, s>>>(a, vec ? 1 : 0);
   return cudaGetLastError();
 }
 
@@ -277,7 +394,11 @@ extern "C" kdv_status kdv_logits_process(const kdv_logits_params* p, void* strea
   a.max_T = p->max_T;
   a.total_nodes = p->total_nodes;
   a.vocab = p->vocab;
-  a.tile = 2048;
+  // Nodes of a CTA: all of a tree once the tiles alone fill the GPU (each more
+  // CTA counts the history again), else as few as are in flight at once.
+  const int64_t tiles = ((int64_t)p->vocab + TILE - 1) / TILE * p->batch;
+  const int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((p->max_T + NODES - 1) / NODES, (4 * 148 + tiles - 1) / tiles));
+  a.chunk = (int)(((p->max_T + chunks - 1) / chunks + NODES - 1) / NODES * NODES);
   const bool vec = rows_aligned(p->logits, p->logits_ld, xe) && rows_aligned(p->out, p->out_ld, ye);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;

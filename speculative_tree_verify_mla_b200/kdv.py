@@ -471,10 +471,13 @@ def _fill(p, kw: dict):
 
 def _launch(fn: str, p, stream) -> None:
     """Call an entry point on the device of the struct's tensors."""
-    f = getattr(load(), fn)
+    f = getattr(_lib or load(), fn)
     dev = getattr(p, "_device", None)
-    if dev is None or dev == torch.cuda.current_device():
-        status = f(ctypes.byref(p), _stream(stream))
+    if dev is None or dev == torch._C._cuda_getDevice():
+        if stream is None and dev is not None:
+            status = f(ctypes.byref(p), torch._C._cuda_getCurrentRawStream(dev) or None)
+        else:
+            status = f(ctypes.byref(p), _stream(stream))
     else:
         with torch.cuda.device(dev):
             status = f(ctypes.byref(p), _stream(stream))
