@@ -57,18 +57,23 @@ using namespace ptx;
 
 constexpr int ROWS = V8_ROWS, KEYS = V8_KEYS, DC = 512, DR = 64;
 constexpr int BLOCK = 16384;                 // 128 keys x 128 bytes, or 128 stacked query rows x 128 bytes
-constexpr int PARTS = 5;                     // blocks of a tile: rope, latent 0..3
+constexpr int BLOCKS = 4;                    // latent blocks of a tile, behind its rope block
 constexpr int RING = 7;
 constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;
 constexpr int KS_BUFS = 4;
 constexpr int GROUPS = 4, GROUP_ROWS = ROWS / GROUPS;       // softmax warpgroups, 16 query rows each
 constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 4;
-constexpr int THREADS = (SOFTMAX_WARPS + 1 + PRODUCER_WARPS) * 32;
+constexpr int FIRST_PRODUCER = MMA_WARP + 4;                // a warpgroup of its own
+constexpr int THREADS = (FIRST_PRODUCER + PRODUCER_WARPS) * 32;
+// registers a thread: 80 at launch, moved from the other two warpgroups to the four of the softmax
+constexpr int LAUNCH_REGS = 80, SOFTMAX_REGS = 88, OTHER_REGS = 64;
+static_assert(SOFTMAX_WARPS * SOFTMAX_REGS + (THREADS / 32 - SOFTMAX_WARPS) * OTHER_REGS <= THREADS / 32 * LAUNCH_REGS, "register split");
 constexpr float P_TOP = 12.f, P_GROW = 15.f; // log2 of the largest p when the reference is set / allowed later
 constexpr float UNIT_ROOM = 4.f;             // how far scales may grow before their unit moves
 constexpr float NO_MAX = -1e30f;             // the reference of a row that has seen no key
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
+constexpr uint32_t POLLS = 64;               // between two looks at the clock
 
 constexpr int OFF_Q = 0;                                   // 4 blocks: rows 0-63 hi, 64-127 lo
 constexpr int OFF_QR = OFF_Q + 4 * BLOCK;                  // rows 0-63 q_rope bf16, 64-127 zero
@@ -82,14 +87,15 @@ constexpr int OFF_RED = OFF_CM + 32 * 16;                  // float [GROUPS][4][
 constexpr int OFF_FAC = OFF_RED + GROUPS * 4 * GROUP_ROWS * 4;   // float [64] per-row factors
 constexpr int OFF_RED2 = OFF_FAC + ROWS * 4;               // float [GROUPS][4]
 constexpr int OFF_BAR = OFF_RED2 + GROUPS * 16;
-constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_KS = B_EMPTY + RING, B_S = B_KS + KS_BUFS, B_P = B_S + 2, B_ROPE = B_P + 1,
-              B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
+constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_KS = B_EMPTY + RING, B_S = B_KS + KS_BUFS, B_P = B_S + 2,
+              B_ROPE = B_P + 1, B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
 constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int SMEM_BYTES = OFF_ABORT + 4 + 1024;
 static_assert(OFF_BAR % 8 == 0 && OFF_MASK % 8 == 0 && OFF_CM % 16 == 0, "alignment");
 static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory");
-constexpr uint32_t TM_S = 256;                             // S buffers behind the 4 x 64 output columns
+constexpr uint32_t TM_S = BLOCKS * ROWS;                   // S buffers behind the output columns
+static_assert(TM_S + 4 * ROWS <= 512, "tensor memory");
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -112,7 +118,7 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_fmt, int b_f
 }
 constexpr uint32_t IDESC_QK = idesc_f8(128, 128, 0, 0, false, false);
 constexpr uint32_t IDESC_ROPE = idesc_bf16_f32(128, 128, false, false);
-constexpr uint32_t IDESC_PV = idesc_f8(128, 64, 0, 1, true, true);
+constexpr uint32_t IDESC_PV = idesc_f8(128, ROWS, 0, 1, true, true);
 
 // 64-byte-swizzled descriptor (P: 64 query rows of a key are one 64-byte row, eight keys a group of 512 bytes)
 __device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -136,20 +142,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" :: "l"(p)); }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+// Arrives on `bar` when all of this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Bounded waits: a wait that runs out reports, raises the CTA's abort flag and
 // returns false; from then on every other wait of the CTA returns at once.
@@ -161,17 +165,22 @@ struct Waiter {
     if (mbar_try(bar, parity)) return true;
     return slow(bar, parity);
   }
-  __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const {
-    const uint64_t t0 = global_ns();
-    while (!mbar_try(bar, parity)) {
+  // (Reading the global timer takes hundreds of clocks, so it is looked at
+  // once in many polls: with one read a poll each wait ended that much late.)
+  __device__ __forceinline__ bool slow(uint32_t bar, uint32_t parity) const {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+      if (mbar_try(bar, parity)) return true;
+      if (n % POLLS != 0) continue;
       if (*abort) return false;
-      if (global_ns() - t0 > limit) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit) {
         *abort = 1;
         record_error(d_err, KDV_DERR_TIMEOUT);
         return false;
       }
     }
-    return true;
   }
 };
 
@@ -307,6 +316,11 @@ __device__ __forceinline__ void split_p(uint32_t h, uint32_t& t0, uint32_t& t1, 
   t2 = c;
 }
 
+// Places of the ring: 0 for the rope block, freed within the tile; the latent
+// blocks, counted over all tiles, rotate through the others.
+__device__ __forceinline__ int latent_place(int n) { return 1 + n % (RING - 1); }
+__device__ __forceinline__ int latent_uses(int n) { return n / (RING - 1); }
+
 __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_constant__ Verify8Args a,
                                                                 const __grid_constant__ VerifyPlan p) {
   extern __shared__ uint8_t raw[];
@@ -343,16 +357,16 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   }
   if (tid == 0) {
     for (int i = 0; i < RING; ++i) {
-      mbar_init(bar(B_FULL + i), PRODUCER_WARPS);
+      mbar_init(bar(B_FULL + i), 32 * PRODUCER_WARPS);
       mbar_init(bar(B_EMPTY + i), 1);
     }
     for (int i = 0; i < KS_BUFS; ++i) mbar_init(bar(B_KS + i), PRODUCER_WARPS);
     mbar_init(bar(B_S), 1);
     mbar_init(bar(B_S + 1), 1);
+    mbar_init(bar(B_FIN), 1);
     mbar_init(bar(B_P), SOFTMAX_WARPS);
     mbar_init(bar(B_ROPE), 1);
     mbar_init(bar(B_Q), SOFTMAX_WARPS);
-    mbar_init(bar(B_FIN), 1);
     *abort = 0;
     fence_mbar_init();
   }
@@ -365,71 +379,68 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sp + OFF_TMEM);
 
-  if (warp > MMA_WARP) {
+  if (warp < SOFTMAX_WARPS) regs_inc<SOFTMAX_REGS>();
+  else regs_dec<OTHER_REGS>();
+
+  if (warp >= FIRST_PRODUCER) {
     // ---------------------------------------------------------- producers
     // Each warp brings its 32 keys of every block, so that a block freed by
-    // P.V is full again as soon as may be; up to INFLIGHT blocks in flight.
+    // P.V is full again as soon as may be. A lane's copies arrive on the block's
+    // barrier by themselves; the fence between them and the tensor cores' reads is the issuing
+    // thread's, behind its wait (a fence here drains the copies in flight: measured 900 clocks a block instead of 350).
     const int64_t kv_base = a.kv_off[b];
-    const int mine = warp - MMA_WARP - 1;            // keys 32 mine .. 32 mine + 31 of a tile
+    const int mine = warp - FIRST_PRODUCER;            // keys 32 mine .. 32 mine + 31 of a tile
     auto load_slot = [&](int tile) {                 // of this lane's key; -1 none, -2 outside the pool
       const int j = k_lo + tile * KEYS + mine * 32 + lane;
       if (tile >= NT || j >= k_hi) return -1;
       const int64_t s = a.page_table ? (int64_t)a.page_table[kv_base + j] : kv_base + j;
       return s >= 0 && s < a.num_slots ? (int)s : -2;
     };
-    constexpr int INFLIGHT = 3;
     const int sub = lane >> 3, col = (lane & 7) * 16;
-    uint32_t dst[8];                                 // of this lane's pieces within a block
-#pragma unroll
-    for (int q = 0; q < 8; ++q) dst[q] = base + OFF_RING + swz128((mine * 32 + q * 4 + sub) * 128 + col);
-    int pos = 0, use = 0, first = 0, pending = 0;    // the next place of the ring; oldest place in flight, how many are
-    auto hand_over = [&](int count) {                // the oldest `count` have landed
-      fence_proxy_async_smem();
-      __syncwarp();
-      for (int x = 0; x < count; ++x) {
-        if (lane == 0) mbar_arrive(bar(B_FULL + first));
-        first = first + 1 == RING ? 0 : first + 1;
-      }
-      pending -= count;
-    };
     // The ring holds little more than a tile, so a block's load starts late;
-    // its rows are asked into L2 two tiles before (a lane its key's five lines).
+    // its rows are asked into L2 two tiles before (a lane its key's lines).
     auto prefetch = [&](int slot) {
       if (slot < 0) return;
       const uint8_t* c = a.c8 + (int64_t)slot * DC;
       prefetch_l2(a.kr + (int64_t)slot * DR);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) prefetch_l2(c + 128 * x);
+      for (int x = 0; x < BLOCKS; ++x) prefetch_l2(c + 128 * x);
     };
     int next = load_slot(0), after = load_slot(1);
     prefetch(after);
-    bool go = true;
-    for (int tile = 0; tile < NT && go; ++tile) {
+    const uint8_t* c8 = a.c8 + col;
+    const uint8_t* kr = reinterpret_cast<const uint8_t*>(a.kr) + col;
+    const uint32_t dst0 = base + OFF_RING + swz128((mine * 32 + sub) * 128 + col);         // rows sub, sub + 8, ..
+    const uint32_t dst1 = base + OFF_RING + swz128((mine * 32 + 4 + sub) * 128 + col);     // rows sub + 4, sub + 12, ..
+    for (int tile = 0; tile < NT; ++tile) {
       const int slot = next;
       next = after;
       after = load_slot(tile + 2);
-      int s[8];
+      uint32_t s[8], take = 0;                       // the slots of this lane's rows; which of them are readable
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s[q] = __shfl_sync(0xffffffffu, slot, q * 4 + sub);
-#pragma unroll 1
-      for (int part = 0; part < PARTS; ++part) {
-        if (use > 0 && !__all_sync(0xffffffffu, mbar_test(bar(B_EMPTY + pos), (use - 1) & 1))) {
-          if (pending > 0) {                         // nothing to add yet: hand over what is in flight
-            cp_async_wait<0>();
-            hand_over(pending);
-          }
-          if (!__all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1))) {
-            go = false;
-            break;
-          }
+      for (int q = 0; q < 8; ++q) {
+        const int x = __shfl_sync(0xffffffffu, slot, q * 4 + sub);
+        s[q] = (uint32_t)max(x, 0);
+        take |= x >= 0 ? 1u << q : 0u;
+      }
+      const bool whole = __all_sync(0xffffffffu, take == 0xffu);
+      const float ks = slot < 0 ? 0.f : a.kv_scale[slot >> a.block_log2];
+      bool go = true;
+#pragma unroll
+      for (int part = 0; part <= BLOCKS; ++part) {
+        const int n = tile * BLOCKS + part - 1;
+        const int pos = part == 0 ? 0 : latent_place(n), use = part == 0 ? tile : latent_uses(n);
+        if (use > 0 && !(go = __all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1)))) break;
+        const uint8_t* src = part == 0 ? kr : c8 + (part - 1) * 128;
+        const uint32_t pitch = part == 0 ? DR * 2 : DC;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t dst = (q % 2 ? dst1 : dst0) + pos * BLOCK + (q / 2) * 1024;
+          if (whole) cp_async16(dst, src + (uint64_t)s[q] * pitch);
+          else cp_async16_or_zero(dst, src + (uint64_t)s[q] * pitch, (take >> q) & 1u ? 16 : 0);
         }
-        const uint8_t* src0 = part == 0 ? reinterpret_cast<const uint8_t*>(a.kr) + col : a.c8 + (part - 1) * 128 + col;
-        const int64_t pitch = part == 0 ? DR * 2 : DC;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) cp_async16(dst[q] + pos * BLOCK, src0 + (s[q] < 0 ? 0 : s[q]) * pitch, s[q] < 0 ? 0 : 16);
-        cp_async_commit();
+        cp_async_arrive(bar(B_FULL + pos));
         if (part == 0) {
-          const float ks = slot < 0 ? 0.f : a.kv_scale[slot >> a.block_log2];
           const uint32_t okw = __ballot_sync(0xffffffffu, slot >= 0);
           reinterpret_cast<float*>(sp + OFF_KS)[(tile % KS_BUFS) * KEYS + mine * 32 + lane] =
               finite(ks) ? ks : __int_as_float(0x7fc00000);              // a row of infinities has NaN logits
@@ -438,107 +449,75 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(B_KS + tile % KS_BUFS));
         }
-        if (part == PARTS - 1) prefetch(after);
-        if (++pending == INFLIGHT) {
-          cp_async_wait<INFLIGHT - 1>();
-          hand_over(1);
-        }
-        if (++pos == RING) {
-          pos = 0;
-          ++use;
-        }
       }
+      if (!go) break;
+      prefetch(after);
     }
-    cp_async_wait<0>();
-    hand_over(pending);
+    cp_async_wait_all();
   } else if (warp == MMA_WARP) {
     // ---------------------------------------------------------- MMA issue
-    if (NT > 0) {
+    // One thread. The pipe takes few MMAs ahead, so the time between two of
+    // them is its idle time. The next tile's rope part and first two latent blocks
+    // run while the softmax works on this tile; its other two wait for the places that
+    // P.V frees, and run between P.V's blocks once they have been filled.
+    if (NT > 0 && elect_one()) {
       const uint64_t q_desc = sw128_desc(base + OFF_Q, 16, 1024), qr_desc = sw128_desc(base + OFF_QR, 16, 1024);
       const uint64_t p_desc = sw64_desc(base + OFF_P, P_BYTES, 512);
       const uint64_t k_desc = sw128_desc(base + OFF_RING, 16, 1024), v_desc = sw128_desc(base + OFF_RING, BLOCK, 1024);
-      auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-      int tile = 0, part = 0, pos = 0, use = 0;      // the next block of Q.K^T
-      auto ready = [&]() { return all(mbar_test(bar(B_FULL + pos), use & 1)); };
-      // Q.K^T of that block (its barrier has been waited for)
-      auto qk = [&]() {
-        const uint64_t kb = k_desc + (uint32_t)(pos * (BLOCK / 16));
-        const uint32_t d = tmem + TM_S + (tile & 1) * 128;
-        bool good = true;
+      auto rope = [&](int i) {
+        if (!wait(bar(B_FULL), i & 1)) return false;
+        fence_proxy_async_smem();
         tc_fence_after();
-        if (part == 0) {
-          // products of two kinds into one accumulator: the second kind waits
-          // for the first (it has the softmax's time for that)
-          if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss(d, kb + 2 * k, qr_desc + 2 * k, IDESC_ROPE, k > 0);
-            tc_commit(bar(B_EMPTY + pos));
-            tc_commit(bar(B_ROPE));
-          }
-          __syncwarp();
-          good = all(wait(bar(B_ROPE), tile & 1));
-        } else {
-          const uint64_t qb = q_desc + (uint32_t)((part - 1) * (BLOCK / 16));
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f8(d, kb + 2 * k, qb + 2 * k, IDESC_QK, 1u);
-          }
-          __syncwarp();
-        }
-        if (++part == PARTS) {
-          part = 0;
-          ++tile;
-        }
-        if (++pos == RING) {
-          pos = 0;
-          ++use;
-        }
-        return good;
+        for (int k = 0; k < 4; ++k) mma_ss(tmem + TM_S + (i & 1) * 128, k_desc + 2 * k, qr_desc + 2 * k, IDESC_ROPE, k > 0);
+        tc_commit(bar(B_EMPTY));
+        tc_commit(bar(B_ROPE));
+        // products of another kind into the same sums wait for these
+        return wait(bar(B_ROPE), i & 1);
       };
-      bool go = all(wait(bar(B_Q), 0));
-      int vpos = 1;                                  // ring place of the next latent block of P.V
-      for (int i = -1; i < NT && go; ++i) {
-        if (i >= 0) {
-          // the next tile's blocks while this tile's numerators are not ready;
-          // the ring holds up to its third
-          while (tile == i + 1 && tile < NT && part < 3 && go && !all(mbar_test(bar(B_P), i & 1))) {
-            if (ready()) go = qk();
-            else if (all(*abort != 0)) go = false;
-          }
-          if (!go || !(go = all(wait(bar(B_P), i & 1)))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
-            const uint64_t vb = v_desc + (uint32_t)(vpos * (BLOCK / 16));
-            if (elect_one()) {
+      auto latent = [&](int i, int x) {
+        const int n = i * BLOCKS + x, at = latent_place(n);
+        const uint64_t kb = k_desc + (uint32_t)(at * (BLOCK / 16)), qb = q_desc + (uint32_t)(x * (BLOCK / 16));
+        if (!wait(bar(B_FULL + at), latent_uses(n) & 1)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
 #pragma unroll
-              for (int t = 0; t < TERMS; ++t)
+        for (int k = 0; k < 4; ++k) mma_f8(tmem + TM_S + (i & 1) * 128, kb + 2 * k, qb + 2 * k, IDESC_QK, 1u);
+        if (x == BLOCKS - 1) tc_commit(bar(B_S + (i & 1)));
+        return true;
+      };
+      auto values = [&](int i, int x) {
+        const int at = latent_place(i * BLOCKS + x);
+        const uint64_t vb = v_desc + (uint32_t)(at * (BLOCK / 16));
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_f8(tmem + mt * 64, vb + k * 256, p_desc + (t * P_BYTES + k * 2048) / 16, IDESC_PV,
-                         (t > 0 || k > 0) ? 1u : (uint32_t)(i > 0));
-              tc_commit(bar(B_EMPTY + vpos));
-            }
-            __syncwarp();
-            vpos = vpos + 1 == RING ? 0 : vpos + 1;
-          }
-          vpos = vpos + 1 == RING ? 0 : vpos + 1;    // over the rope block
-        }
-        if (i + 1 < NT) {
-          while (tile == i + 1 && go) go = all(wait(bar(B_FULL + pos), use & 1)) && qk();
-          if (go && elect_one()) tc_commit(bar(B_S + ((i + 1) & 1)));
-          __syncwarp();
-        }
+        for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f8(tmem + x * ROWS, vb + k * 256, p_desc + (t * P_BYTES + k * 2048) / 16, IDESC_PV,
+                   t > 0 || k > 0 ? 1u : (uint32_t)(i > 0));
+        tc_commit(bar(B_EMPTY + at));
+      };
+      bool go = wait(bar(B_Q), 0) && rope(0) && latent(0, 0) && latent(0, 1) && latent(0, 2) && latent(0, 3);
+      for (int i = 0; i < NT && go; ++i) {
+        const bool more = i + 1 < NT;
+        if (more && !(go = rope(i + 1) && latent(i + 1, 0) && latent(i + 1, 1))) break;
+        if (!(go = wait(bar(B_P), i & 1))) break;
+        tc_fence_after();
+        values(i, 0);
+        values(i, 1);
+        values(i, 2);
+        if (more && !(go = latent(i + 1, 2))) break;
+        values(i, 3);
+        if (more) go = latent(i + 1, 3);
       }
       // nothing of this CTA may still run when its tensor memory is given
       // back: a wait of its own, whatever happened before
-      if (elect_one()) tc_commit(bar(B_FIN));
-      __syncwarp();
+      tc_commit(bar(B_FIN));
       const uint64_t t0 = global_ns();
       while (!mbar_try(bar(B_FIN), 0) && global_ns() - t0 < TIMEOUT_NS) {}
     }
     __syncwarp();
-  } else {
+  } else if (warp < SOFTMAX_WARPS) {
     // ------------------------------------------------- queries and softmax
     const int g = warp >> 2, w = warp & 3;           // warpgroup, lane quarter
     float4* cm = reinterpret_cast<float4*>(sp + OFF_CM) + g * (GROUP_ROWS / 2);    // this group's
@@ -583,13 +562,13 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       const bool plain = __all_sync(0xffffffffu, readable && u < 0);
       wait(bar(B_S + (i & 1)), (i >> 1) & 1);
       tc_fence_after();
-      float t[16];
+      float t[16], d[16];
       bool dirty;
-      auto scores = [&]() {                          // t = s_j (q . k), -inf where the row does not see the key
+      {                                              // t = s_j (q . k), -inf where the row does not see the key
         uint32_t hi[16], lo[16];
         const uint32_t sb = quarter + TM_S + (i & 1) * 128 + GROUP_ROWS * g;
         tmem_ld16(sb, hi);
-        tmem_ld16(sb + 64, lo);
+        tmem_ld16(sb + ROWS, lo);
         tmem_wait_ld();
         dirty = isnan(__uint_as_float(lo[0]));
 #pragma unroll
@@ -607,27 +586,26 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
             t[r] = vis ? t[r] : -INFINITY;
           }
         }
-      };
-      auto exponents = [&]() {                       // t = log2 of the numerators; the largest
+      }
+      auto exponents = [&]() {                       // d = log2 of the numerators; the largest
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
           const float4 f = cm[r / 2];
-          const float2 d = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
-          t[r] = d.x;
-          t[r + 1] = d.y;
-          top = fmaxf(top, fmaxf(d.x, d.y));
+          const float2 x = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(f.z, f.w));
+          d[r] = x.x;
+          d[r + 1] = x.y;
+          top = fmaxf(top, fmaxf(x.x, x.y));
         }
         return top;
       };
-      scores();
       // The low terms of a query are finite whatever the query holds, so a NaN
       // in their sums is the key's: its row of V becomes zeros, or 0 * NaN would
       // reach rows that do not see it. (Rows that see it get their NaN from p.)
       if (dirty) {
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt) {
-          uint4* v = reinterpret_cast<uint4*>(sp + OFF_RING + ((i * PARTS + 1 + mt) % RING) * BLOCK + key * 128);
+        for (int mt = 0; mt < BLOCKS; ++mt) {
+          uint4* v = reinterpret_cast<uint4*>(sp + OFF_RING + latent_place(i * BLOCKS + mt) * BLOCK + key * 128);
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
         }
       }
@@ -635,14 +613,13 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       const bool move = i == 0 || exponents() > P_GROW || fabsf(s) > unit;
       if (i == 0 || named_bar_or(wg_bar, 128, move)) {
         // ---- some reference moves: maxima over the tile's keys, per row
-        if (i > 0) scores();
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
           const float4 f = cm[r / 2];
-          t[r] *= f.x;
-          t[r + 1] *= f.y;
+          d[r] = t[r] * f.x;
+          d[r + 1] = t[r + 1] * f.y;
         }
-        const float mine = transpose_reduce(t, lane, [](float x, float y) { return fmaxf(x, y); });   // of row `lane`
+        const float mine = transpose_reduce(d, lane, [](float x, float y) { return fmaxf(x, y); });   // of row `lane`
         if (lane < GROUP_ROWS) red[w * GROUP_ROWS + lane] = mine;
         const float smax = warp_max(isnan(s) ? 0.f : fabsf(s));
         if (lane == 0) red2[w] = smax;
@@ -676,17 +653,16 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 #pragma unroll
           for (int r = 0; r < 16; ++r) l[r] *= fac[r];
 #pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int x = 0; x < BLOCKS; ++x) {
             uint32_t o[16];
-            tmem_ld16(quarter + mt * 64 + GROUP_ROWS * g, o);
+            tmem_ld16(quarter + x * ROWS + GROUP_ROWS * g, o);
             tmem_wait_ld();
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * (fac[r] * us));
-            tmem_st16(quarter + mt * 64 + GROUP_ROWS * g, o);
+            tmem_st16(quarter + x * ROWS + GROUP_ROWS * g, o);
           }
           tmem_wait_st();
         }
-        scores();
         exponents();
       }
       const float sr = s * inv_unit;
@@ -697,7 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const int r = 4 * q4 + 2 * k;
-          const float p0 = ex2(t[r]), p1 = ex2(t[r + 1]);
+          const float p0 = ex2(d[r]), p1 = ex2(d[r + 1]);
           const float2 sum = add_f32x2(make_float2(l[r], l[r + 1]), make_float2(p0, p1));
           l[r] = sum.x;
           l[r + 1] = sum.y;
@@ -753,11 +729,11 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       constexpr int LINE = 128 * sizeof(T), PER = LINE / 16;
       uint8_t* out = static_cast<uint8_t*>(dst) + orow0 * 4 * LINE;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt) {
+      for (int mt = 0; mt < BLOCKS; ++mt) {
         T* buf = reinterpret_cast<T*>(stage + (mt & 1) * (GROUP_ROWS * 512));
         uint32_t o[16];
         if (NT > 0) {
-          tmem_ld16(quarter + mt * 64 + GROUP_ROWS * g, o);
+          tmem_ld16(quarter + mt * ROWS + GROUP_ROWS * g, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
