@@ -506,9 +506,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         values(i, 0);
         values(i, 1);
         values(i, 2);
-        if (more && !(go = latent(i + 1, 2))) break;
         values(i, 3);
-        if (more) go = latent(i + 1, 3);
+        if (more) go = latent(i + 1, 2) && latent(i + 1, 3);
       }
       // nothing of this CTA may still run when its tensor memory is given
       // back: a wait of its own, whatever happened before
