@@ -59,7 +59,7 @@ constexpr int ROWS = V8_ROWS, KEYS = V8_KEYS, DC = 512, DR = 64;
 constexpr int BLOCK = 16384;                 // 128 keys x 128 bytes, or 128 stacked query rows x 128 bytes
 constexpr int BLOCKS = 4;                    // latent blocks of a tile, behind its rope block
 constexpr int RING = 7;
-constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;
+constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;   // terms of a numerator (a fill, a use and a last use of V's operand)
 constexpr int KS_BUFS = 4;
 constexpr int GROUPS = 4, GROUP_ROWS = ROWS / GROUPS;       // softmax warpgroups, 16 query rows each
 constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 4;
@@ -97,11 +97,21 @@ static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory");
 constexpr uint32_t TM_S = BLOCKS * ROWS;                   // S buffers behind the output columns
 static_assert(TM_S + 4 * ROWS <= 512, "tensor memory");
 
+// KEEP: what happens to A in the tensor core's operand buffer. Three MMAs in
+// a row with the same A read it from shared memory once: 36 clocks each (M 128, N 64), 48 without.
+enum class A { ONCE, FILL, USE, LAST };
+template <A KEEP = A::ONCE>
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+#define KDV_MMA_F8(COLLECT) \
+  asm volatile( \
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t" \
+      "tcgen05.mma.cta_group::1.kind::f8f6f4" COLLECT " [%0], %1, %2, %3, p;\n\t}" \
+      :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory")
+  if constexpr (KEEP == A::FILL) KDV_MMA_F8(".collector::a::fill");
+  else if constexpr (KEEP == A::USE) KDV_MMA_F8(".collector::a::use");
+  else if constexpr (KEEP == A::LAST) KDV_MMA_F8(".collector::a::lastuse");
+  else KDV_MMA_F8("");
+#undef KDV_MMA_F8
 }
 // One lane of a converged warp, the same at every call. The issuing warp runs
 // its loop with all lanes and elects around each block of MMAs: measured 48 clocks an
@@ -489,12 +499,14 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       auto values = [&](int i, int x) {
         const int at = latent_place(i * BLOCKS + x);
         const uint64_t vb = v_desc + (uint32_t)(at * (BLOCK / 16));
+        const uint32_t d = tmem + x * ROWS;
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f8(tmem + x * ROWS, vb + k * 256, p_desc + (t * P_BYTES + k * 2048) / 16, IDESC_PV,
-                   t > 0 || k > 0 ? 1u : (uint32_t)(i > 0));
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t v = vb + k * 256, p = p_desc + k * (2048 / 16);
+          mma_f8<A::FILL>(d, v, p, IDESC_PV, k > 0 ? 1u : (uint32_t)(i > 0));
+          mma_f8<A::USE>(d, v, p + P_BYTES / 16, IDESC_PV, 1u);
+          mma_f8<A::LAST>(d, v, p + 2 * P_BYTES / 16, IDESC_PV, 1u);
+        }
         tc_commit(bar(B_EMPTY + at));
       };
       bool go = wait(bar(B_Q), 0) && rope(0) && latent(0, 0) && latent(0, 1) && latent(0, 2) && latent(0, 3);
