@@ -60,14 +60,10 @@ constexpr int BLOCK = 16384;                 // 128 keys x 128 bytes, or 128 sta
 constexpr int BLOCKS = 4;                    // latent blocks of a tile, behind its rope block
 constexpr int RING = 7;
 constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;   // terms of a numerator (a fill, a use and a last use of V's operand)
-constexpr int KS_BUFS = 4;
 constexpr int GROUPS = 4, GROUP_ROWS = ROWS / GROUPS;       // softmax warpgroups, 16 query rows each
-constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 4;
-constexpr int FIRST_PRODUCER = MMA_WARP + 4;                // a warpgroup of its own
-constexpr int THREADS = (FIRST_PRODUCER + PRODUCER_WARPS) * 32;
-// registers a thread: 80 at launch, moved from the other two warpgroups to the four of the softmax
-constexpr int LAUNCH_REGS = 80, SOFTMAX_REGS = 88, OTHER_REGS = 64;
-static_assert(SOFTMAX_WARPS * SOFTMAX_REGS + (THREADS / 32 - SOFTMAX_WARPS) * OTHER_REGS <= THREADS / 32 * LAUNCH_REGS, "register split");
+constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 3;
+constexpr int FIRST_PRODUCER = MMA_WARP + 1;
+constexpr int THREADS = (FIRST_PRODUCER + PRODUCER_WARPS) * 32;   // 640: 96 registers a thread
 constexpr float P_TOP = 12.f, P_GROW = 15.f; // log2 of the largest p when the reference is set / allowed later
 constexpr float UNIT_ROOM = 4.f;             // how far scales may grow before their unit moves
 constexpr float NO_MAX = -1e30f;             // the reference of a row that has seen no key
@@ -79,15 +75,13 @@ constexpr int OFF_Q = 0;                                   // 4 blocks: rows 0-6
 constexpr int OFF_QR = OFF_Q + 4 * BLOCK;                  // rows 0-63 q_rope bf16, 64-127 zero
 constexpr int OFF_P = OFF_QR + BLOCK;
 constexpr int OFF_RING = OFF_P + TERMS * P_BYTES;
-constexpr int OFF_KS = OFF_RING + RING * BLOCK;            // float [KS_BUFS][128] key scales
-constexpr int OFF_OK = OFF_KS + KS_BUFS * KEYS * 4;        // u32 [KS_BUFS][4] readable keys
-constexpr int OFF_MASK = OFF_OK + KS_BUFS * 16;            // u64 [64] node masks by row
+constexpr int OFF_MASK = OFF_RING + RING * BLOCK;          // u64 [64] node masks by row
 constexpr int OFF_CM = OFF_MASK + ROWS * 8;                // float4 [32]: (c, c', -m, -m') of a row pair
 constexpr int OFF_RED = OFF_CM + 32 * 16;                  // float [GROUPS][4][16]
 constexpr int OFF_FAC = OFF_RED + GROUPS * 4 * GROUP_ROWS * 4;   // float [64] per-row factors
 constexpr int OFF_RED2 = OFF_FAC + ROWS * 4;               // float [GROUPS][4]
 constexpr int OFF_BAR = OFF_RED2 + GROUPS * 16;
-constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_KS = B_EMPTY + RING, B_S = B_KS + KS_BUFS, B_P = B_S + 2,
+constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_S = B_EMPTY + RING, B_P = B_S + 2,
               B_ROPE = B_P + 1, B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
 constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
@@ -151,9 +145,6 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -370,7 +361,6 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       mbar_init(bar(B_FULL + i), 32 * PRODUCER_WARPS);
       mbar_init(bar(B_EMPTY + i), 1);
     }
-    for (int i = 0; i < KS_BUFS; ++i) mbar_init(bar(B_KS + i), PRODUCER_WARPS);
     mbar_init(bar(B_S), 1);
     mbar_init(bar(B_S + 1), 1);
     mbar_init(bar(B_FIN), 1);
@@ -389,52 +379,38 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sp + OFF_TMEM);
 
-  if (warp < SOFTMAX_WARPS) regs_inc<SOFTMAX_REGS>();
-  else regs_dec<OTHER_REGS>();
-
+  // A key's pool slot in two steps, so that nothing waits for the page table
+  // where it is read: its entry, and a tile later what that means (-1 no key, -2 outside the pool).
+  const int64_t kv_base = a.kv_off[b];
+  auto entry_of = [&](int j) { return j >= k_hi ? -1 : a.page_table ? a.page_table[kv_base + j] : (int)(kv_base + j); };
+  auto slot_of = [&](int j, int entry) { return j >= k_hi ? -1 : entry >= 0 && entry < a.num_slots ? entry : -2; };
   if (warp >= FIRST_PRODUCER) {
     // ---------------------------------------------------------- producers
-    // Each warp brings its 32 keys of every block, so that a block freed by
-    // P.V is full again as soon as may be. A lane's copies arrive on the block's
+    // Every warp brings a third of each block (four rows a copy), so that a block freed
+    // by P.V is full again as soon as may be. A lane's copies arrive on the block's
     // barrier by themselves; the fence between them and the tensor cores' reads is the issuing
     // thread's, behind its wait (a fence here drains the copies in flight: measured 900 clocks a block instead of 350).
-    const int64_t kv_base = a.kv_off[b];
-    const int mine = warp - FIRST_PRODUCER;            // keys 32 mine .. 32 mine + 31 of a tile
-    auto load_slot = [&](int tile) {                 // of this lane's key; -1 none, -2 outside the pool
-      const int j = k_lo + tile * KEYS + mine * 32 + lane;
-      if (tile >= NT || j >= k_hi) return -1;
-      const int64_t s = a.page_table ? (int64_t)a.page_table[kv_base + j] : kv_base + j;
-      return s >= 0 && s < a.num_slots ? (int)s : -2;
-    };
-    const int sub = lane >> 3, col = (lane & 7) * 16;
-    // The ring holds little more than a tile, so a block's load starts late;
-    // its rows are asked into L2 two tiles before (a lane its key's lines).
-    auto prefetch = [&](int slot) {
-      if (slot < 0) return;
-      const uint8_t* c = a.c8 + (int64_t)slot * DC;
-      prefetch_l2(a.kr + (int64_t)slot * DR);
+    constexpr int COPIES = (KEYS / 4 + PRODUCER_WARPS - 1) / PRODUCER_WARPS;
+    const int mine = warp - FIRST_PRODUCER, sub = lane >> 3, col = (lane & 7) * 16;
+    auto row = [&](int q) { return (mine + PRODUCER_WARPS * q) * 4 + sub; };
+    int next[COPIES];                                // this lane's rows in the page table, read a tile ahead
+    auto load_slots = [&](int tile) {
 #pragma unroll
-      for (int x = 0; x < BLOCKS; ++x) prefetch_l2(c + 128 * x);
+      for (int q = 0; q < COPIES; ++q) next[q] = row(q) < KEYS ? entry_of(k_lo + tile * KEYS + row(q)) : -1;
     };
-    int next = load_slot(0), after = load_slot(1);
-    prefetch(after);
     const uint8_t* c8 = a.c8 + col;
     const uint8_t* kr = reinterpret_cast<const uint8_t*>(a.kr) + col;
-    const uint32_t dst0 = base + OFF_RING + swz128((mine * 32 + sub) * 128 + col);         // rows sub, sub + 8, ..
-    const uint32_t dst1 = base + OFF_RING + swz128((mine * 32 + 4 + sub) * 128 + col);     // rows sub + 4, sub + 12, ..
+    const uint32_t ring = base + OFF_RING;
+    load_slots(0);
     for (int tile = 0; tile < NT; ++tile) {
-      const int slot = next;
-      next = after;
-      after = load_slot(tile + 2);
-      uint32_t s[8], take = 0;                       // the slots of this lane's rows; which of them are readable
+      uint32_t s[COPIES], take = 0;                  // which rows are readable; the others become zeros
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int x = __shfl_sync(0xffffffffu, slot, q * 4 + sub);
-        s[q] = (uint32_t)max(x, 0);
-        take |= x >= 0 ? 1u << q : 0u;
+      for (int q = 0; q < COPIES; ++q) {
+        const int slot = slot_of(k_lo + tile * KEYS + row(q), next[q]);
+        s[q] = (uint32_t)max(slot, 0);
+        take |= slot >= 0 ? 1u << q : 0u;
       }
-      const bool whole = __all_sync(0xffffffffu, take == 0xffu);
-      const float ks = slot < 0 ? 0.f : a.kv_scale[slot >> a.block_log2];
+      load_slots(tile + 1);
       bool go = true;
 #pragma unroll
       for (int part = 0; part <= BLOCKS; ++part) {
@@ -444,24 +420,13 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         const uint8_t* src = part == 0 ? kr : c8 + (part - 1) * 128;
         const uint32_t pitch = part == 0 ? DR * 2 : DC;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t dst = (q % 2 ? dst1 : dst0) + pos * BLOCK + (q / 2) * 1024;
-          if (whole) cp_async16(dst, src + (uint64_t)s[q] * pitch);
-          else cp_async16_or_zero(dst, src + (uint64_t)s[q] * pitch, (take >> q) & 1u ? 16 : 0);
+        for (int q = 0; q < COPIES; ++q) {
+          if (row(q) < KEYS)
+            cp_async16_or_zero(ring + pos * BLOCK + swz128(row(q) * 128 + col), src + (uint64_t)s[q] * pitch, (take >> q) & 1u ? 16 : 0);
         }
         cp_async_arrive(bar(B_FULL + pos));
-        if (part == 0) {
-          const uint32_t okw = __ballot_sync(0xffffffffu, slot >= 0);
-          reinterpret_cast<float*>(sp + OFF_KS)[(tile % KS_BUFS) * KEYS + mine * 32 + lane] =
-              finite(ks) ? ks : __int_as_float(0x7fc00000);              // a row of infinities has NaN logits
-          if (lane == 0) reinterpret_cast<uint32_t*>(sp + OFF_OK)[(tile % KS_BUFS) * 4 + mine] = okw;
-          if (slot == -2) record_error(a.d_err, KDV_DERR_BAD_SLOT);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_KS + tile % KS_BUFS));
-        }
       }
       if (!go) break;
-      prefetch(after);
     }
     cp_async_wait_all();
   } else if (warp == MMA_WARP) {
@@ -564,12 +529,27 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     const int key = w * 32 + lane;
     uint8_t* prow = sp + OFF_P + key * ROWS + (((uint32_t)g ^ (((uint32_t)key >> 1) & 3u)) << 4);   // 64-byte swizzle
 
+    // This key's scale is read a tile ahead, its slot two. The ring holds little more
+    // than a tile, so a block's copies start late: its rows are asked into L2 when their
+    // slots are known, a 128-byte line by each group (and not by the copying warps, where the
+    // requests of random rows back up: 900 to 2200 clocks a tile).
+    auto scale_of = [&](int slot) { return slot < 0 ? 0.f : a.kv_scale[slot >> a.block_log2]; };
+    auto prefetch = [&](int slot) {
+      if (slot < 0) return;
+      prefetch_l2(a.c8 + (int64_t)slot * DC + 128 * g);
+      if (g == 0) prefetch_l2(static_cast<const __nv_bfloat16*>(a.kr) + (int64_t)slot * DR);
+    };
+    int slot = entry_of(k_lo + key), slot_next = entry_of(k_lo + KEYS + key), entry = entry_of(k_lo + 2 * KEYS + key);
+    slot = slot_of(k_lo + key, slot);
+    slot_next = slot_of(k_lo + KEYS + key, slot_next);
+    float ks = scale_of(slot), ks_next = scale_of(slot_next);
+    prefetch(slot_next);
+
     for (int i = 0; i < NT; ++i) {
-      wait(bar(B_KS + i % KS_BUFS), (i / KS_BUFS) & 1);
-      const float s = reinterpret_cast<const float*>(sp + OFF_KS)[(i % KS_BUFS) * KEYS + key];
-      const uint32_t okw = reinterpret_cast<const uint32_t*>(sp + OFF_OK)[(i % KS_BUFS) * 4 + w];
+      if (g == 0 && slot == -2) record_error(a.d_err, KDV_DERR_BAD_SLOT);
+      const float s = finite(ks) ? ks : __int_as_float(0x7fc00000);   // a row of infinities has NaN logits
+      const bool readable = slot >= 0;
       const int u = k_lo + i * KEYS + key - L;       // tree key if >= 0
-      const bool readable = (okw >> lane) & 1u;
       const bool plain = __all_sync(0xffffffffu, readable && u < 0);
       wait(bar(B_S + (i & 1)), (i >> 1) & 1);
       tc_fence_after();
@@ -706,6 +686,12 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_P));
+      slot = slot_next;
+      ks = ks_next;
+      slot_next = slot_of(k_lo + (i + 2) * KEYS + key, entry);
+      ks_next = scale_of(slot_next);
+      prefetch(slot_next);
+      entry = entry_of(k_lo + (i + 3) * KEYS + key);
     }
 
     if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");   // the merge's launch overlaps the rest
