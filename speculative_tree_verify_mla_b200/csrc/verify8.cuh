@@ -36,7 +36,7 @@ struct Verify8Args {
 };
 
 constexpr int V8_ROWS = 64;      // query rows of a tensor-core work item
-constexpr int V8_KEYS = 128;     // keys of a tile
+constexpr int V8_KEYS = 96;      // keys of its tiles
 
 // mask word of node t
 __device__ inline uint64_t node_mask(const Verify8Args& a, const VerifyPlan& p, int b, int t) {

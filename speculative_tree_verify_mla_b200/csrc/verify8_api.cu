@@ -79,7 +79,7 @@ int64_t parts_of(const VerifyPlan& v) {
 }
 size_t part_o_bytes(const VerifyPlan& v, int d) { return align256((size_t)parts_of(v) * d * (v.part_f16 ? 2 : 4)); }
 
-// Work items and splits. Splits cover whole 128-key tiles. Automatic: the
+// Work items and splits. Splits cover whole key tiles. Automatic: the
 // chunk of X keys that minimises a cost in keys of one item: one wave of
 // items costs its longest, X + C; more waves their total over the SMs plus
 // half an item for the ragged end. C is an item's fixed cost (queries,
@@ -118,7 +118,7 @@ kdv_status make_plan(const kdv_verify8_params* p, int impl, VerifyPlan* v, size_
     const double n = items_for(X);
     return n <= slots ? X + C : (work + n * C) / slots + 0.5 * (X + C);
   };
-  const int64_t align = SPLIT_ALIGN, x_hi = (max_n + align - 1) / align * align;
+  const int64_t align = tc ? V8_KEYS : SPLIT_ALIGN, x_hi = (max_n + align - 1) / align * align;
   int64_t X = x_hi;
   double best = cost(x_hi);
   for (double xf = (double)align; xf < (double)x_hi; xf = std::max(xf * 1.04, xf + align)) {

@@ -56,9 +56,10 @@ namespace {
 using namespace ptx;
 
 constexpr int ROWS = V8_ROWS, KEYS = V8_KEYS, DC = 512, DR = 64;
-constexpr int BLOCK = 16384;                 // 128 keys x 128 bytes, or 128 stacked query rows x 128 bytes
+constexpr int QBLOCK = 16384;                // 128 stacked query rows x 128 bytes
+constexpr int BLOCK = KEYS * 128;            // a tile's keys x 128 bytes
 constexpr int BLOCKS = 4;                    // latent blocks of a tile, behind its rope block
-constexpr int RING = 7;
+constexpr int ROPE_PLACES = 2, RING = ROPE_PLACES + 2 * BLOCKS;   // two tiles
 constexpr int TERMS = 3, P_BYTES = KEYS * ROWS;   // terms of a numerator (a fill, a use and a last use of V's operand)
 constexpr int GROUPS = 4, GROUP_ROWS = ROWS / GROUPS;       // softmax warpgroups, 16 query rows each
 constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 3;
@@ -72,9 +73,10 @@ constexpr uint64_t TIMEOUT_NS = 1000000000ull;
 constexpr uint32_t POLLS = 64;               // between two looks at the clock
 
 constexpr int OFF_Q = 0;                                   // 4 blocks: rows 0-63 hi, 64-127 lo
-constexpr int OFF_QR = OFF_Q + 4 * BLOCK;                  // rows 0-63 q_rope bf16, 64-127 zero
-constexpr int OFF_P = OFF_QR + BLOCK;
+constexpr int OFF_QR = OFF_Q + 4 * QBLOCK;                 // rows 0-63 q_rope bf16, 64-127 zero
+constexpr int OFF_P = OFF_QR + QBLOCK;
 constexpr int OFF_RING = OFF_P + TERMS * P_BYTES;
+// an MMA reads 128 rows of a block: the last one's end is 4 KB further
 constexpr int OFF_MASK = OFF_RING + RING * BLOCK;          // u64 [64] node masks by row
 constexpr int OFF_CM = OFF_MASK + ROWS * 8;                // float4 [32]: (c, c', -m, -m') of a row pair
 constexpr int OFF_RED = OFF_CM + 32 * 16;                  // float [GROUPS][4][16]
@@ -82,10 +84,11 @@ constexpr int OFF_FAC = OFF_RED + GROUPS * 4 * GROUP_ROWS * 4;   // float [64] p
 constexpr int OFF_RED2 = OFF_FAC + ROWS * 4;               // float [GROUPS][4]
 constexpr int OFF_BAR = OFF_RED2 + GROUPS * 16;
 constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_S = B_EMPTY + RING, B_P = B_S + 2,
-              B_ROPE = B_P + 1, B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
+              B_PV = B_P + 1, B_ROPE = B_PV + 1, B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
 constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
-constexpr int SMEM_BYTES = OFF_ABORT + 4 + 1024;
+constexpr int SMEM_BYTES = (OFF_ABORT + 4 > OFF_MASK + (128 - KEYS) * 128 ? OFF_ABORT + 4 : OFF_MASK + (128 - KEYS) * 128) + 1024;
+static_assert(KEYS == 96 && KEYS * ROWS % 512 == 0, "tile");
 static_assert(OFF_BAR % 8 == 0 && OFF_MASK % 8 == 0 && OFF_CM % 16 == 0, "alignment");
 static_assert(SMEM_BYTES <= 232448, "exceeds 227 KB of shared memory");
 constexpr uint32_t TM_S = BLOCKS * ROWS;                   // S buffers behind the output columns
@@ -265,7 +268,7 @@ struct QueryRow {
       }
       lo[i] = e4m3x4(y[0], y[1], y[2], y[3]);
     }
-    const uint32_t blk = (uint32_t)(lane / 8) * BLOCK, col = (uint32_t)(lane % 8) * 16;
+    const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     const float ra = __uint_as_float(rope << 16) * up, rb = __uint_as_float(rope & 0xffff0000u) * up;
@@ -317,10 +320,9 @@ __device__ __forceinline__ void split_p(uint32_t h, uint32_t& t0, uint32_t& t1, 
   t2 = c;
 }
 
-// Places of the ring: 0 for the rope block, freed within the tile; the latent
-// blocks, counted over all tiles, rotate through the others.
-__device__ __forceinline__ int latent_place(int n) { return 1 + n % (RING - 1); }
-__device__ __forceinline__ int latent_uses(int n) { return n / (RING - 1); }
+// Places of the ring: rope blocks alternate between two, latent blocks between two sets.
+__device__ __forceinline__ int rope_place(int tile) { return tile & 1; }
+__device__ __forceinline__ int latent_place(int tile, int x) { return ROPE_PLACES + (tile & 1) * BLOCKS + x; }
 
 __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_constant__ Verify8Args a,
                                                                 const __grid_constant__ VerifyPlan p) {
@@ -363,6 +365,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     }
     mbar_init(bar(B_S), 1);
     mbar_init(bar(B_S + 1), 1);
+    mbar_init(bar(B_PV), 1);
     mbar_init(bar(B_FIN), 1);
     mbar_init(bar(B_P), SOFTMAX_WARPS);
     mbar_init(bar(B_ROPE), 1);
@@ -390,13 +393,14 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     // by P.V is full again as soon as may be. A lane's copies arrive on the block's
     // barrier by themselves; the fence between them and the tensor cores' reads is the issuing
     // thread's, behind its wait (a fence here drains the copies in flight: measured 900 clocks a block instead of 350).
-    constexpr int COPIES = (KEYS / 4 + PRODUCER_WARPS - 1) / PRODUCER_WARPS;
+    constexpr int COPIES = KEYS / 4 / PRODUCER_WARPS;
+    static_assert(COPIES * PRODUCER_WARPS * 4 == KEYS, "a warp's share of a block");
     const int mine = warp - FIRST_PRODUCER, sub = lane >> 3, col = (lane & 7) * 16;
     auto row = [&](int q) { return (mine + PRODUCER_WARPS * q) * 4 + sub; };
     int next[COPIES];                                // this lane's rows in the page table, read a tile ahead
     auto load_slots = [&](int tile) {
 #pragma unroll
-      for (int q = 0; q < COPIES; ++q) next[q] = row(q) < KEYS ? entry_of(k_lo + tile * KEYS + row(q)) : -1;
+      for (int q = 0; q < COPIES; ++q) next[q] = entry_of(k_lo + tile * KEYS + row(q));
     };
     const uint8_t* c8 = a.c8 + col;
     const uint8_t* kr = reinterpret_cast<const uint8_t*>(a.kr) + col;
@@ -414,16 +418,13 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       bool go = true;
 #pragma unroll
       for (int part = 0; part <= BLOCKS; ++part) {
-        const int n = tile * BLOCKS + part - 1;
-        const int pos = part == 0 ? 0 : latent_place(n), use = part == 0 ? tile : latent_uses(n);
+        const int pos = part == 0 ? rope_place(tile) : latent_place(tile, part - 1), use = tile >> 1;
         if (use > 0 && !(go = __all_sync(0xffffffffu, wait(bar(B_EMPTY + pos), (use - 1) & 1)))) break;
         const uint8_t* src = part == 0 ? kr : c8 + (part - 1) * 128;
         const uint32_t pitch = part == 0 ? DR * 2 : DC;
 #pragma unroll
-        for (int q = 0; q < COPIES; ++q) {
-          if (row(q) < KEYS)
-            cp_async16_or_zero(ring + pos * BLOCK + swz128(row(q) * 128 + col), src + (uint64_t)s[q] * pitch, (take >> q) & 1u ? 16 : 0);
-        }
+        for (int q = 0; q < COPIES; ++q)
+          cp_async16_or_zero(ring + pos * BLOCK + swz128(row(q) * 128 + col), src + (uint64_t)s[q] * pitch, (take >> q) & 1u ? 16 : 0);
         cp_async_arrive(bar(B_FULL + pos));
       }
       if (!go) break;
@@ -432,41 +433,46 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   } else if (warp == MMA_WARP) {
     // ---------------------------------------------------------- MMA issue
     // One thread. The pipe takes few MMAs ahead, so the time between two of
-    // them is its idle time. The next tile's rope part and first two latent blocks
-    // run while the softmax works on this tile; its other two wait for the places that
-    // P.V frees, and run between P.V's blocks once they have been filled.
+    // them is its idle time: blocks of MMAs are long and their waits lie behind others.
+    // P.V of tile i, then Q.K^T of tile i + 2, while the softmax works on tile i + 1. (Products of
+    // another kind into the same sums wait for the rope part's end, which P.V's last block covers.)
     if (NT > 0 && elect_one()) {
       const uint64_t q_desc = sw128_desc(base + OFF_Q, 16, 1024), qr_desc = sw128_desc(base + OFF_QR, 16, 1024);
       const uint64_t p_desc = sw64_desc(base + OFF_P, P_BYTES, 512);
       const uint64_t k_desc = sw128_desc(base + OFF_RING, 16, 1024), v_desc = sw128_desc(base + OFF_RING, BLOCK, 1024);
       auto rope = [&](int i) {
-        if (!wait(bar(B_FULL), i & 1)) return false;
+        const int at = rope_place(i);
+        if (!wait(bar(B_FULL + at), (i >> 1) & 1)) return false;
         fence_proxy_async_smem();
         tc_fence_after();
+        const uint64_t kb = k_desc + (uint32_t)(at * (BLOCK / 16));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_ss(tmem + TM_S + (i & 1) * 128, k_desc + 2 * k, qr_desc + 2 * k, IDESC_ROPE, k > 0);
-        tc_commit(bar(B_EMPTY));
+        for (int k = 0; k < 4; ++k) mma_ss(tmem + TM_S + (i & 1) * 128, kb + 2 * k, qr_desc + 2 * k, IDESC_ROPE, k > 0);
+        tc_commit(bar(B_EMPTY + at));
         tc_commit(bar(B_ROPE));
-        // products of another kind into the same sums wait for these
-        return wait(bar(B_ROPE), i & 1);
+        return true;
       };
-      auto latent = [&](int i, int x) {
-        const int n = i * BLOCKS + x, at = latent_place(n);
-        const uint64_t kb = k_desc + (uint32_t)(at * (BLOCK / 16)), qb = q_desc + (uint32_t)(x * (BLOCK / 16));
-        if (!wait(bar(B_FULL + at), latent_uses(n) & 1)) return false;
-        fence_proxy_async_smem();
-        tc_fence_after();
+      auto latents = [&](int i) {
+        if (!wait(bar(B_ROPE), i & 1)) return false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_f8(tmem + TM_S + (i & 1) * 128, kb + 2 * k, qb + 2 * k, IDESC_QK, 1u);
-        if (x == BLOCKS - 1) tc_commit(bar(B_S + (i & 1)));
+        for (int x = 0; x < BLOCKS; ++x) {
+          const int at = latent_place(i, x);
+          const uint64_t kb = k_desc + (uint32_t)(at * (BLOCK / 16)), qb = q_desc + (uint32_t)(x * (QBLOCK / 16));
+          if (!wait(bar(B_FULL + at), (i >> 1) & 1)) return false;
+          fence_proxy_async_smem();
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f8(tmem + TM_S + (i & 1) * 128, kb + 2 * k, qb + 2 * k, IDESC_QK, 1u);
+        }
+        tc_commit(bar(B_S + (i & 1)));
         return true;
       };
       auto values = [&](int i, int x) {
-        const int at = latent_place(i * BLOCKS + x);
+        const int at = latent_place(i, x);
         const uint64_t vb = v_desc + (uint32_t)(at * (BLOCK / 16));
         const uint32_t d = tmem + x * ROWS;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < KEYS / 32; ++k) {
           const uint64_t v = vb + k * 256, p = p_desc + k * (2048 / 16);
           mma_f8<A::FILL>(d, v, p, IDESC_PV, k > 0 ? 1u : (uint32_t)(i > 0));
           mma_f8<A::USE>(d, v, p + P_BYTES / 16, IDESC_PV, 1u);
@@ -474,17 +480,19 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         }
         tc_commit(bar(B_EMPTY + at));
       };
-      bool go = wait(bar(B_Q), 0) && rope(0) && latent(0, 0) && latent(0, 1) && latent(0, 2) && latent(0, 3);
+      bool go = wait(bar(B_Q), 0);
+      for (int i = 0; i < 2 && i < NT && go; ++i) go = rope(i) && latents(i);
       for (int i = 0; i < NT && go; ++i) {
-        const bool more = i + 1 < NT;
-        if (more && !(go = rope(i + 1) && latent(i + 1, 0) && latent(i + 1, 1))) break;
+        const bool more = i + 2 < NT;
         if (!(go = wait(bar(B_P), i & 1))) break;
         tc_fence_after();
         values(i, 0);
         values(i, 1);
         values(i, 2);
+        if (more) go = rope(i + 2);
         values(i, 3);
-        if (more) go = latent(i + 1, 2) && latent(i + 1, 3);
+        tc_commit(bar(B_PV));
+        if (more) go = go && latents(i + 2);
       }
       // nothing of this CTA may still run when its tensor memory is given
       // back: a wait of its own, whatever happened before
@@ -526,7 +534,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     for (int i = 0; i < 16; ++i) l[i] = 0.f;
     float unit = 0.f, inv_unit = 0.f;                // the power of two that s_j is taken relative to
     const uint32_t quarter = tmem + ((uint32_t)(w * 32) << 16);
-    const int key = w * 32 + lane;
+    const int key = w * 32 + lane;                   // also the dim of a block; the last quarter has no keys
+    const int no_key = key < KEYS ? 0 : 1 << 30;     // added to a key that there is not
     uint8_t* prow = sp + OFF_P + key * ROWS + (((uint32_t)g ^ (((uint32_t)key >> 1) & 3u)) << 4);   // 64-byte swizzle
 
     // This key's scale is read a tile ahead, its slot two. The ring holds little more
@@ -539,9 +548,9 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       prefetch_l2(a.c8 + (int64_t)slot * DC + 128 * g);
       if (g == 0) prefetch_l2(static_cast<const __nv_bfloat16*>(a.kr) + (int64_t)slot * DR);
     };
-    int slot = entry_of(k_lo + key), slot_next = entry_of(k_lo + KEYS + key), entry = entry_of(k_lo + 2 * KEYS + key);
-    slot = slot_of(k_lo + key, slot);
-    slot_next = slot_of(k_lo + KEYS + key, slot_next);
+    int slot = entry_of(k_lo + key + no_key), slot_next = entry_of(k_lo + KEYS + key + no_key), entry = entry_of(k_lo + 2 * KEYS + key + no_key);
+    slot = slot_of(k_lo + key + no_key, slot);
+    slot_next = slot_of(k_lo + KEYS + key + no_key, slot_next);
     float ks = scale_of(slot), ks_next = scale_of(slot_next);
     prefetch(slot_next);
 
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         tmem_ld16(sb, hi);
         tmem_ld16(sb + ROWS, lo);
         tmem_wait_ld();
-        dirty = isnan(__uint_as_float(lo[0]));
+        dirty = key < KEYS && isnan(__uint_as_float(lo[0]));
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
           float2 x = fma_f32x2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), make_float2(0.0625f, 0.0625f),
@@ -596,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       if (dirty) {
 #pragma unroll 1
         for (int mt = 0; mt < BLOCKS; ++mt) {
-          uint4* v = reinterpret_cast<uint4*>(sp + OFF_RING + latent_place(i * BLOCKS + mt) * BLOCK + key * 128);
+          uint4* v = reinterpret_cast<uint4*>(sp + OFF_RING + latent_place(i, mt) * BLOCK + key * 128);
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
         }
       }
@@ -640,7 +649,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         unit = unit_new;
         inv_unit = 1.f / unit_new;
         if (i > 0) {
-          // P.V of the tiles before is complete: this tile's S was committed behind it
+          wait(bar(B_PV), (i - 1) & 1);              // P.V of the tiles before is complete
+          tc_fence_after();
 #pragma unroll
           for (int r = 0; r < 16; ++r) l[r] *= fac[r];
 #pragma unroll 1
@@ -679,19 +689,22 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         w1[q4] = __byte_perm(t1[0], t1[1], 0x7531);
         w2[q4] = t2[0] | (t2[1] << 16);
       }
-      *reinterpret_cast<uint4*>(prow) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-      *reinterpret_cast<uint4*>(prow + P_BYTES) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
-      *reinterpret_cast<uint4*>(prow + 2 * P_BYTES) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+      if (i > 0) wait(bar(B_PV), (i - 1) & 1);       // the numerators' place is free
+      if (key < KEYS) {
+        *reinterpret_cast<uint4*>(prow) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+        *reinterpret_cast<uint4*>(prow + P_BYTES) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        *reinterpret_cast<uint4*>(prow + 2 * P_BYTES) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_P));
       slot = slot_next;
       ks = ks_next;
-      slot_next = slot_of(k_lo + (i + 2) * KEYS + key, entry);
+      slot_next = slot_of(k_lo + (i + 2) * KEYS + key + no_key, entry);
       ks_next = scale_of(slot_next);
       prefetch(slot_next);
-      entry = entry_of(k_lo + (i + 3) * KEYS + key);
+      entry = entry_of(k_lo + (i + 3) * KEYS + key + no_key);
     }
 
     if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");   // the merge's launch overlaps the rest
