@@ -132,10 +132,11 @@ kdv_status make_plan(const kdv_verify8_params* p, int impl, VerifyPlan* v, size_
   bool all_one = true;
   for (int b = 0; b < B; ++b) {
     const int64_t n = (int64_t)v->L[b] + v->T[b];
-    const int64_t S = p->num_splits >= 1 ? p->num_splits : (n + X - 1) / X;
+    int64_t S = p->num_splits >= 1 ? p->num_splits : (n + X - 1) / X;
     if (S > 4096) return KDV_ERR_UNSUPPORTED;
-    v->S[b] = (int32_t)S;
     v->chunk[b] = (int32_t)(align * ((n + align * S - 1) / (align * S)));
+    if (p->num_splits == 0) S = (n + v->chunk[b] - 1) / v->chunk[b];   // whole tiles may need fewer
+    v->S[b] = (int32_t)S;
     v->item_base[b] = (int32_t)items;
     v->part_base[b] = (int32_t)parts;
     items += (int64_t)v->tiles[b] * S;

@@ -189,16 +189,15 @@ struct Waiter {
 };
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t f16x2) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(f16x2));
+  return c;
 }
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t c) {
+__device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return h;
 }
 // largest x of a warp, through the order-preserving integer image of a float
 __device__ __forceinline__ float warp_max(float x) {
@@ -243,30 +242,28 @@ struct QueryRow {
     // the power of two that brings the largest element into [128, 256)
     const int e = top == 0u ? 0 : max(-120, min(60, 7 + 127 - (int)(top >> 7)));
     const float up = __int_as_float((e + 127) << 23);
+    // (fp16 holds the scaled elements: exact down to 2^-14, off by 2^-25 at most below)
     uint32_t hi[4], lo[4];
+    const __half2 sixteen = __float2half2_rn(16.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x[4], y[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        x[2 * j] = __uint_as_float(u[2 * i + j] << 16) * up;
-        x[2 * j + 1] = __uint_as_float(u[2 * i + j] & 0xffff0000u) * up;
+        float x0 = __uint_as_float(u[2 * i + j] << 16) * up, x1 = __uint_as_float(u[2 * i + j] & 0xffff0000u) * up;
+        if (bad) {
+          x0 = finite(x0) ? x0 : __int_as_float(0x7fc00000);
+          x1 = finite(x1) ? x1 : __int_as_float(0x7fc00000);
+        }
+        const uint32_t x = pack_f16x2(x0, x1), h = e4m3x2(x), back = e4m3x2_f16(h);
+        __half2 y = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&back)), sixteen);
+        if (bad) {                                   // the low terms stay finite, see the softmax
+          y.x = __hisnan(y.x) ? __half(0.f) : y.x;
+          y.y = __hisnan(y.y) ? __half(0.f) : y.y;
+        }
+        const uint32_t l = e4m3x2(*reinterpret_cast<const uint32_t*>(&y));
+        hi[i] = j == 0 ? h : hi[i] | (h << 16);
+        lo[i] = j == 0 ? l : lo[i] | (l << 16);
       }
-      if (bad) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = finite(x[j]) ? x[j] : __int_as_float(0x7fc00000);
-      }
-      hi[i] = e4m3x4(x[0], x[1], x[2], x[3]);
-      const float2 h01 = e4m3x2_values(hi[i] & 0xffffu), h23 = e4m3x2_values(hi[i] >> 16);
-      y[0] = 16.f * (x[0] - h01.x);
-      y[1] = 16.f * (x[1] - h01.y);
-      y[2] = 16.f * (x[2] - h23.x);
-      y[3] = 16.f * (x[3] - h23.y);
-      if (bad) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = isnan(y[j]) ? 0.f : y[j];   // the low terms stay finite, see the softmax
-      }
-      lo[i] = e4m3x4(y[0], y[1], y[2], y[3]);
     }
     const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -334,6 +331,25 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   volatile int* abort = reinterpret_cast<volatile int*>(sp + OFF_ABORT);
   const Waiter wait{abort, a.d_err, a.wait_limit_ns ? a.wait_limit_ns : TIMEOUT_NS};
 
+  if (tid == FIRST_PRODUCER * 32) {
+    for (int i = 0; i < RING; ++i) {
+      mbar_init(bar(B_FULL + i), 32 * PRODUCER_WARPS);
+      mbar_init(bar(B_EMPTY + i), 1);
+    }
+    mbar_init(bar(B_S), 1);
+    mbar_init(bar(B_S + 1), 1);
+    mbar_init(bar(B_PV), 1);
+    mbar_init(bar(B_FIN), 1);
+    mbar_init(bar(B_P), SOFTMAX_WARPS);
+    mbar_init(bar(B_ROPE), 1);
+    mbar_init(bar(B_Q), SOFTMAX_WARPS);
+    *abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(base + OFF_TMEM, 512);
+    tmem_relinquish();
+  }
   const int item = blockIdx.x;
   const int b = plan_request(p, item);
   const int local = item - p.item_base[b];
@@ -357,25 +373,6 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       row[k].load(q + ((int64_t)p.tree_base[b] * p.H + lr) * a.q_row_stride, lr < rows_b, lane);
       if (lane == 0 && lr < rows_b) qmask[k] = node_mask(a, p, b, lr / p.H);
     }
-  }
-  if (tid == 0) {
-    for (int i = 0; i < RING; ++i) {
-      mbar_init(bar(B_FULL + i), 32 * PRODUCER_WARPS);
-      mbar_init(bar(B_EMPTY + i), 1);
-    }
-    mbar_init(bar(B_S), 1);
-    mbar_init(bar(B_S + 1), 1);
-    mbar_init(bar(B_PV), 1);
-    mbar_init(bar(B_FIN), 1);
-    mbar_init(bar(B_P), SOFTMAX_WARPS);
-    mbar_init(bar(B_ROPE), 1);
-    mbar_init(bar(B_Q), SOFTMAX_WARPS);
-    *abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == MMA_WARP) {
-    tmem_alloc(base + OFF_TMEM, 512);
-    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -738,28 +735,31 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       using T = decltype(zero);
       constexpr int LINE = 128 * sizeof(T), PER = LINE / 16;
       uint8_t* out = static_cast<uint8_t*>(dst) + orow0 * 4 * LINE;
+      float f[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) f[r] = fac[r];
+      uint32_t o[16], ahead[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[r] = ahead[r] = 0u;
+      if (NT > 0) {
+        tmem_ld16(quarter + GROUP_ROWS * g, o);
+        tmem_wait_ld();
+      }
 #pragma unroll
       for (int mt = 0; mt < BLOCKS; ++mt) {
         T* buf = reinterpret_cast<T*>(stage + (mt & 1) * (GROUP_ROWS * 512));
-        uint32_t o[16];
-        if (NT > 0) {
-          tmem_ld16(quarter + mt * ROWS + GROUP_ROWS * g, o);
-          tmem_wait_ld();
-        } else {
+        if (NT > 0 && mt + 1 < BLOCKS) tmem_ld16(quarter + (mt + 1) * ROWS + GROUP_ROWS * g, ahead);
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[r] = 0u;
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float f = fac[r];
-          buf[r * 128 + key] = convert(f == 0.f ? 0.f : __uint_as_float(o[r]) * f);
-        }
+        for (int r = 0; r < 16; ++r) buf[r * 128 + key] = convert(f[r] == 0.f ? 0.f : __uint_as_float(o[r]) * f[r]);
         named_bar_sync(wg_bar, 128);                 // the other buffer's readers have passed the barrier before this one
 #pragma unroll
         for (int x = key; x < GROUP_ROWS * PER; x += 128) {
           const int r = x / PER, c = x % PER;
           if (r < nr) reinterpret_cast<uint4*>(out + (r * 4 + mt) * LINE)[c] = reinterpret_cast<const uint4*>(buf + r * 128)[c];
         }
+        if (NT > 0) tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[r] = ahead[r];
       }
     };
     if (!direct) write(__half(), [](float v) { return __float2half_rn(v); }, a.part_o);
