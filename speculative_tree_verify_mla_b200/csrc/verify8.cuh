@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "kdv_internal.cuh"
 
 namespace kdv {
@@ -50,6 +52,19 @@ __device__ inline bool request_ok(const Verify8Args& a, const VerifyPlan& p, int
   if (report && (!ok || (a.prefix_len != nullptr && a.prefix_len[b] != p.L[b]) || a.tree_off[b] != p.tree_base[b]))
     record_error(a.d_err, KDV_DERR_BAD_LENGTH);
   return ok;
+}
+
+// Raises a kernel's dynamic shared memory limit, once for each device.
+inline cudaError_t allow_smem(const void* kernel, int bytes) {
+  static std::atomic<uint64_t> done[4];                    // devices below 256
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 256;
+  if (known && (done[dev / 64].load(std::memory_order_acquire) >> (dev % 64)) & 1u) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
+  return e;
 }
 
 cudaError_t launch_verify8_simt(const Verify8Args& a, const VerifyPlan& p, cudaStream_t stream);

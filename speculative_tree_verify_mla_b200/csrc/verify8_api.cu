@@ -111,7 +111,7 @@ kdv_status make_plan(const kdv_verify8_params* p, int impl, VerifyPlan* v, size_
   const double C = tc ? 384.0 : 128.0;
   auto items_for = [&](int64_t X) {
     double n = 0.0;
-    for (int b = 0; b < B; ++b) n += (double)v->tiles[b] * (double)(((int64_t)v->L[b] + v->T[b] + X - 1) / X);
+    for (int b = 0; b < B; ++b) n += (double)v->tiles[b] * (double)((uint32_t)(v->L[b] + v->T[b] + X - 1) / (uint32_t)X);
     return n;
   };
   auto cost = [&](int64_t X) {
@@ -121,7 +121,7 @@ kdv_status make_plan(const kdv_verify8_params* p, int impl, VerifyPlan* v, size_
   const int64_t align = tc ? V8_KEYS : SPLIT_ALIGN, x_hi = (max_n + align - 1) / align * align;
   int64_t X = x_hi;
   double best = cost(x_hi);
-  for (double xf = (double)align; xf < (double)x_hi; xf = std::max(xf * 1.04, xf + align)) {
+  for (double xf = (double)align; xf < (double)x_hi; xf = std::max(xf * 1.05, xf + align)) {
     const int64_t x = (int64_t)xf / align * align;
     if (cost(x) < best) {
       best = cost(x);

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
   while (b + 1 < p.B && p.tree_base[b + 1] * p.H <= row) ++b;
   const int rows_b = p.T[b] * p.H, r = row - p.tree_base[b] * p.H, S = p.S[b];
   const int64_t base = p.part_base[b] + r;
+  asm volatile("griddepcontrol.launch_dependents;");       // the next launch may prepare itself
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the attention kernel's parts
   float m = -INFINITY;
   bool bad = false;                       // a NaN part makes the row NaN

@@ -352,6 +352,8 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   }
   const int item = blockIdx.x;
   const int b = plan_request(p, item);
+  // The launch overlaps the end of the kernel before it on the stream; from here on its results are read.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int local = item - p.item_base[b];
   const int split = local / p.tiles[b], rt = local - split * p.tiles[b];
   const int L = p.L[b], n_keys = L + p.T[b], rows_b = p.T[b] * p.H;
@@ -774,10 +776,20 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 }  // namespace
 
 cudaError_t launch_verify8_tc(const Verify8Args& a, const VerifyPlan& p, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(verify8_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(verify8_tc_kernel), SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  verify8_tc_kernel<<<p.n_items, THREADS, SMEM_BYTES, stream>>>(a, p);
-  return cudaGetLastError();
+  // a programmatic dependent: it waits itself, before its first read
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.n_items);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify8_tc_kernel, a, p);
 }
 
 }  // namespace kdv
