@@ -14,8 +14,8 @@
 // bias at all and streams the logits, two nodes in flight, the first two asked for before the history is read. Drafted tokens are not counted into the table:
 // each one in the tile has a number there, and a small matrix says how often
 // node t's path holds it, so the nodes need no barrier between them.
-// 13 nodes of 163840 tokens with 5553 of history: 10 us (38 with the tile's nodes one after
-// another and the path counted in and out around each); 160 nodes in fp32: 67 us (87).
+// 13 nodes of 163840 tokens with 5553 of history: 9.5 us (38 with the tile's nodes one after
+// another and the path counted in and out around each); 160 nodes in fp32: 58 us (87).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -28,7 +28,7 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int TOKENS = 8;                  // tokens a thread holds
 constexpr int TILE = THREADS * TOKENS;     // tokens a CTA holds
-constexpr int NODES = 2;                   // nodes in flight
+constexpr int NODES = 2;                   // a CTA's nodes at least: one in hand, one on its way
 
 struct LogitsArgs {
   const void* x;
@@ -110,13 +110,13 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// grid (tiles, batch, chunks of nodes). VEC: rows of both sides 16-byte
+// grid (batch, tiles, chunks of nodes). VEC: rows of both sides 16-byte
 // aligned and the tile whole; the launch's other tiles (the last one) take the scalar form.
 template <typename TX, typename TY, bool VEC>
 __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* count, float* bias, uint8_t* number,
                                              uint8_t (*times)[KDV_MAX_TREE], int* par, int* tok) {
-  const int tid = threadIdx.x, b = blockIdx.y, v0 = blockIdx.x * TILE, n = min(TILE, a.vocab - v0);
-  const bool reports = blockIdx.x == 0 && blockIdx.z == 0;  // what every CTA of the request sees
+  const int tid = threadIdx.x, b = blockIdx.x, v0 = blockIdx.y * TILE, n = min(TILE, a.vocab - v0);
+  const bool reports = blockIdx.y == 0 && blockIdx.z == 0;  // what every CTA of the request sees
   // the request's scalars, all asked for at once
   const int t0 = a.tree_off[b], T = a.tree_off[b + 1] - t0;
   int len = a.hist ? a.hist_len[b] : 0;
@@ -137,7 +137,7 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
     if (a.allow == nullptr) return nullptr;
     const int row = a.allow_row ? a.allow_row[t0 + t] : t0 + t;
     if (row >= a.allow_rows) {
-      if (blockIdx.x == 0 && tid == 0) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
+      if (blockIdx.y == 0 && tid == 0) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
       return nullptr;
     }
     return row < 0 ? nullptr : a.allow + (int64_t)row * a.allow_ld + v0 / 32;
@@ -158,17 +158,10 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
     node_parent = a.parent[t0 + tid];
     node_token = a.token[t0 + tid];
   }
-  Row<TX, VEC> r[NODES];
-  uint32_t bits[NODES];
-  auto load = [&](int t) {
-#pragma unroll
-    for (int k = 0; k < NODES; ++k)
-      if (t + k < last) {
-        r[k].load(x + (int64_t)(t + k) * a.x_ld, n);
-        bits[k] = bits_of(allowed(t + k));
-      }
-  };
-  load(first);
+  Row<TX, VEC> r, ahead;
+  uint32_t bits = 0xffu, bits_ahead = 0xffu;
+  r.load(x + (int64_t)first * a.x_ld, n);
+  bits = bits_of(allowed(first));
 
   for (int i = tid; i < TILE / 4; i += THREADS) {
     reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
@@ -207,21 +200,35 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
       len = (int)min((int64_t)max(len, 0), a.hist_ld);
     }
     const int32_t* h = a.hist + b * a.hist_ld;
-    constexpr int FLIGHT = 8;
-    for (int64_t base = tid; base < len; base += THREADS * FLIGHT) {
-      int k[FLIGHT];
+    auto add = [&](uint32_t i, uint32_t at) {
+      if (at < (uint32_t)n) {
+        if ((int)i < pl) atomicOr(&count[at], 1u); else atomicAdd(&count[at], 2u);
+      }
+    };
+    // Nearly every token is another tile's: four at a time, one branch for them all.
+    const uint32_t fours = reinterpret_cast<uintptr_t>(h) % 16 == 0 ? (uint32_t)len / 4 : 0u;
+    constexpr int FLIGHT = 4;
+    for (uint32_t base = tid; base < fours; base += THREADS * FLIGHT) {
+      int4 k[FLIGHT];
 #pragma unroll
-      for (int j = 0; j < FLIGHT; ++j) k[j] = base + j * THREADS < len ? h[base + j * THREADS] : v0 - 1;
+      for (int j = 0; j < FLIGHT; ++j)
+        k[j] = base + j * THREADS < fours ? reinterpret_cast<const int4*>(h)[base + j * THREADS] : make_int4(v0 - 1, v0 - 1, v0 - 1, v0 - 1);
 #pragma unroll
       for (int j = 0; j < FLIGHT; ++j) {
-        const int64_t i = base + j * THREADS;
-        if (reports && i < len && (k[j] < 0 || k[j] >= a.vocab)) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
-        const uint32_t at = (uint32_t)k[j] - (uint32_t)v0;
-        if (i < len && at < (uint32_t)n) {
-          if (i < pl) atomicOr(&count[at], 1u); else atomicAdd(&count[at], 2u);
+        const uint32_t i = 4 * (base + j * THREADS);
+        const uint32_t w = (uint32_t)k[j].x - v0, x = (uint32_t)k[j].y - v0, y = (uint32_t)k[j].z - v0, z = (uint32_t)k[j].w - v0;
+        if (min(min(w, x), min(y, z)) < (uint32_t)n) {
+          add(i, w);
+          add(i + 1, x);
+          add(i + 2, y);
+          add(i + 3, z);
         }
       }
     }
+    for (uint32_t i = 4 * fours + tid; i < (uint32_t)len; i += THREADS) add(i, (uint32_t)h[i] - v0);
+    if (reports)
+      for (uint32_t i = tid; i < (uint32_t)len; i += THREADS)
+        if (h[i] < 0 || h[i] >= a.vocab) record_error(a.d_err, KDV_DERR_BAD_TOKEN);
   }
   // biases: ascending tokens, so the tile's entries are one range
   if (a.bias_off != nullptr) {
@@ -267,22 +274,23 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
   // x / rep as a product where 1 / rep is a normal number (an fp32 rounding more)
   const float inv = 1.f / rep;
   const bool normal = inv >= 1.17549435e-38f && inv <= 3.402823466e38f;
-  for (int t = first; t < last; t += NODES) {
-    if (t > first) load(t);
-    float f[NODES][TOKENS];
+  for (int t = first; t < last; ++t) {
+    if (t + 1 < last) {
+      ahead.load(x + (int64_t)(t + 1) * a.x_ld, n);
+      bits_ahead = bits_of(allowed(t + 1));
+    }
+    float f[TOKENS];
 #pragma unroll
-    for (int k = 0; k < NODES; ++k)
-#pragma unroll
-      for (int j = 0; j < TOKENS; ++j) f[k][j] = r[k].get(j);
+    for (int j = 0; j < TOKENS; ++j) f[j] = r.get(j);
     if (touched != 0) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {                         // four tokens at a time
         uint32_t w[4], id[4] = {0, 0, 0, 0};
         float add[4];
         if (VEC) {
-          const uint4 x = reinterpret_cast<const uint4*>(count)[2 * tid + q];
+          const uint4 c = reinterpret_cast<const uint4*>(count)[2 * tid + q];
           const float4 z = reinterpret_cast<const float4*>(bias)[2 * tid + q];
-          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          w[0] = c.x; w[1] = c.y; w[2] = c.z; w[3] = c.w;
           add[0] = z.x; add[1] = z.y; add[2] = z.z; add[3] = z.w;
           if (drafted) {
             const uint32_t u = reinterpret_cast<const uint32_t*>(number)[2 * tid + q];
@@ -298,31 +306,27 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
           }
         }
 #pragma unroll
-        for (int k = 0; k < NODES; ++k) {
-          if (t + k >= last) break;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t word = id[j] != 0 ? w[j] + 2u * times[t + k][id[j] - 1] : w[j];
-            f[k][4 * q + j] = process(f[k][4 * q + j], word, add[j], rep, inv, normal, pres, freq);
-          }
+        for (int j = 0; j < 4; ++j) {
+          if (id[j] != 0) w[j] += 2u * times[t][id[j] - 1];
+          f[4 * q + j] = process(f[4 * q + j], w[j], add[j], rep, inv, normal, pres, freq);
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < NODES; ++k) {
-      if (t + k >= last) break;
+    if (bits != 0xffu) {
 #pragma unroll
       for (int j = 0; j < TOKENS; ++j)
-        if (!((bits[k] >> j) & 1u)) f[k][j] = __int_as_float(0xff800000);
-      TY* row = y + (int64_t)(t + k) * a.y_ld;
-      if (VEC) {
-        store8(row + TOKENS * tid, f[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < TOKENS; ++j)
-          if (at(j) < n) row[at(j)] = (TY)f[k][j];
-      }
+        if (!((bits >> j) & 1u)) f[j] = __int_as_float(0xff800000);
     }
+    TY* row = y + (int64_t)t * a.y_ld;
+    if (VEC) {
+      store8(row + TOKENS * tid, f);
+    } else {
+#pragma unroll
+      for (int j = 0; j < TOKENS; ++j)
+        if (at(j) < n) row[at(j)] = (TY)f[j];
+    }
+    r = ahead;
+    bits = bits_ahead;
   }
 }
 
@@ -332,13 +336,13 @@ __global__ void __launch_bounds__(THREADS, 4) logits_process_kernel(const __grid
   __shared__ __align__(16) float bias[TILE];
   __shared__ __align__(16) uint8_t number[TILE], times[KDV_MAX_TREE][KDV_MAX_TREE];
   __shared__ int par[KDV_MAX_TREE], tok[KDV_MAX_TREE];
-  if (vec && (int)(blockIdx.x + 1) * TILE <= a.vocab) process_tile<TX, TY, true>(a, count, bias, number, times, par, tok);
+  if (vec && (int64_t)(blockIdx.y + 1) * TILE <= a.vocab) process_tile<TX, TY, true>(a, count, bias, number, times, par, tok);
   else process_tile<TX, TY, false>(a, count, bias, number, times, par, tok);
 }
 
 template <typename TX, typename TY>
 cudaError_t launch_logits(const LogitsArgs& a, int batch, bool vec, cudaStream_t s) {
-  const dim3 grid((unsigned)((a.vocab + TILE - 1) / TILE), (unsigned)batch, (unsigned)((a.max_T + a.chunk - 1) / a.chunk));
+  const dim3 grid((unsigned)batch, (unsigned)(((int64_t)a.vocab + TILE - 1) / TILE), (unsigned)((a.max_T + a.chunk - 1) / a.chunk));
   logits_process_kernel<TX, TY><<<grid, THREADS, 0, s>>>(a, vec ? 1 : 0);
   return cudaGetLastError();
 }
@@ -354,7 +358,7 @@ using namespace kdv;
 
 extern "C" kdv_status kdv_logits_process(const kdv_logits_params* p, void* stream) {
   if (p == nullptr || p->batch < 1 || p->max_T < 1 || p->total_nodes < 0 || p->vocab < 1) return KDV_ERR_INVALID_ARG;
-  if (p->batch > KDV_MAX_BATCH || p->max_T > KDV_MAX_TREE) return KDV_ERR_UNSUPPORTED;
+  if (p->batch > KDV_MAX_BATCH || p->max_T > KDV_MAX_TREE || p->vocab > 65535 * TILE) return KDV_ERR_UNSUPPORTED;
   if ((p->dtype != KDV_BF16 && p->dtype != KDV_F32) || (p->out_dtype != KDV_BF16 && p->out_dtype != KDV_F32))
     return KDV_ERR_INVALID_ARG;
   if (p->logits_ld < p->vocab || p->out_ld < p->vocab) return KDV_ERR_INVALID_ARG;
