@@ -23,28 +23,31 @@
 // of an MMA and 64 query rows as its columns (N): one token of 64 heads fills
 // a tile, where rows of queries would leave half of M = 128 empty, and the fp32
 // output (64 columns for each of four 128-dim blocks) takes 256 columns of
-// TMEM instead of all 512. The same 16 KB block of 128 keys x 128 dims in the
-// 128-byte swizzle is A of Q.K^T (K-major) and A of P.V (M-major).
+// TMEM instead of all 512. The same block of keys x 128 dims in the
+// 128-byte swizzle is A of Q.K^T (K-major) and A of P.V (M-major). The three terms' MMAs of P.V
+// have the same A one after another, which the tensor core keeps: 36 clocks an MMA instead of 48.
 //
 // One CTA per work item: 64 query rows of one request, one key split, tiles
-// of 128 keys:
-//   warps 9-12  producers: gather 128-byte row pieces through the page table
-//               with cp.async into a ring of seven 16 KB blocks (a tile is
-//               the rope block and four latent blocks), one warp a block, four
-//               in flight. (tile::gather4 issues one 512-byte gather in ~65
-//               cycles on this part, 8 B/clk; cp.async beside these MMAs
-//               reached 28 B/clk, of the 20 B/clk that the MMAs consume.)
-//   warp 8      MMA issue: the next tile's Q.K^T (as far as its blocks are
-//               here and the ring holds them) runs while the softmax works on this tile;
-//               then P.V; a block is freed by the last MMA that reads it.
-//   warps 0-7   two warpgroups: queries in, softmax, output. Lane = key, so a
-//               warpgroup owns 32 query rows, a thread one key of them; a row's
+// of 96 keys. (The queries take 80 KB of shared memory. Beside them two tiles of 96
+// fit, so that the softmax of one runs during P.V of the one before and Q.K^T of the one behind; two
+// of 128 do not, and 16 nodes over 200k keys took 502 us instead of 468. The MMAs' rows 96-127 are
+// whatever follows a block; nothing reads what they give.)
+//   warps 17-19 producers: gather 128-byte row pieces through the page table
+//               with cp.async into a ring of ten 12 KB blocks (two rope blocks,
+//               two tiles of four latent blocks), each warp a third of every block.
+//               (tile::gather4 issues one 512-byte gather in ~65 clocks, 8 B/clk;
+//               cp.async beside these MMAs reaches ~28 B/clk.)
+//   warp 16     MMA issue, one thread.
+//   warps 0-15  four warpgroups: queries in, softmax, output. Lane = key, so a
+//               warpgroup owns 16 query rows, a thread one key of them; a row's
 //               maximum is only looked for across lanes when some logit passes
 //               the reference by 2^3 (a vote), then O is rescaled in TMEM.
 //
-// What bounds it: shared-memory reads of the MMAs. Per tile 16 (N = 128) + 4
-// + 48 (N = 64) MMAs of 64, 64 and 48 cycles at 128 B/clk: 3.6k cycles, the
-// same as 82 KB of HBM at this SM's share of 6.46 TB/s.
+// What bounds it: the tensor core and shared memory. A tile's 16 (N = 128) + 4 + 36 (N = 64) MMAs take
+// 2.55k clocks alone and 3.3k beside the copies and the softmax; one cp.async block of 12 KB takes
+// ~400. Over 200k keys the part runs into its power cap: 468 us in bursts, 537 us sustained (16
+// nodes x 64 heads, 952 and 830 TFLOP/s of the logical products). Few rows over short contexts: 16k clocks an item
+// for set-up, queries, first tile and output, and the merge (4-7 us).
 #include <cuda_fp8.h>
 
 #include "sm100_ptx.cuh"
@@ -70,7 +73,8 @@ constexpr float UNIT_ROOM = 4.f;             // how far scales may grow before t
 constexpr float NO_MAX = -1e30f;             // the reference of a row that has seen no key
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
-constexpr uint32_t POLLS = 64;               // between two looks at the clock
+constexpr uint32_t POLLS = 64;               // between two looks at the clock,
+constexpr uint64_t SHORT_NS = 100000;        // unless the limit is shorter than they may take
 
 constexpr int OFF_Q = 0;                                   // 4 blocks: rows 0-63 hi, 64-127 lo
 constexpr int OFF_QR = OFF_Q + 4 * QBLOCK;                 // rows 0-63 q_rope bf16, 64-127 zero
@@ -175,7 +179,7 @@ struct Waiter {
     uint64_t t0 = 0;
     for (uint32_t n = 1;; ++n) {
       if (mbar_try(bar, parity)) return true;
-      if (n % POLLS != 0) continue;
+      if (n % POLLS != 0 && limit >= SHORT_NS) continue;
       if (*abort) return false;
       const uint64_t now = global_ns();
       if (t0 == 0) t0 = now;

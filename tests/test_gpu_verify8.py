@@ -72,6 +72,7 @@ def test_simt_types_and_dims(q_dtype, D_c, D_r, paged):
 SHAPES = [
     ([0], [1], 64), ([1], [1], 16), ([127], [1], 64), ([128], [1], 1), ([126, 127, 128, 129], [1, 1, 1, 1], 8),
     ([300], [13], 64), ([5], [64], 5), ([700, 0, 33], [3, 64, 7], 16), ([1000], [2], 128), ([255], [16], 17),
+    ([95], [1], 64), ([96], [1], 33), ([94, 95, 96, 97], [1, 2, 1, 3], 8), ([191, 192], [64, 1], 3), ([190], [4], 64),
 ]
 
 
@@ -314,3 +315,37 @@ def test_writes_just_before_are_seen():
 def test_long_context():
     c = plain8.Attn(21, [40000], [[-1]], 16, paged=False)
     Run(c).go().check()
+
+
+def test_many_short_requests():
+    """The largest batch, lengths around a tile's, single tokens."""
+    c = plain8.Attn(24, [i % 5 * 48 for i in range(128)], [[-1]] * 128, 16)
+    Run(c).go().check()
+    Run(c, chain=True, out=torch.bfloat16).go().check()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """Waits limited to 1 ns end the call with an error; the next call is right. The same without splits."""
+    c = plain8.Attn(25, [3000], [tree(4)], 64)
+    for splits in (0, 1):
+        good = Run(c, TC, splits=splits).go().check()
+        r = Run(c, TC, splits=splits, wait_limit_ns=1).go()
+        torch.cuda.synchronize()
+        assert r.err.item() == kdv.KDV_DERR_TIMEOUT
+        again = Run(c, TC, splits=splits).go()
+        assert torch.equal(again.o, good.o) and torch.equal(again.lse, good.lse)
+
+
+def test_calls_back_to_back_share_a_workspace():
+    """A call's launch overlaps the end of the call before it: the same workspace and outputs, other inputs."""
+    cases = [plain8.Attn(26 + k, [1500 + 300 * k], [tree(3)], 64, paged=False) for k in range(3)]
+    runs = [Run(c) for c in cases]
+    size = max(r.ws.numel() for r in runs)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    for r in runs:
+        r.p.workspace, r.p.workspace_bytes = ws.data_ptr(), size
+    for _ in range(5):
+        for r in runs:
+            r.go()
+    for r in runs:
+        r.check()

@@ -139,7 +139,8 @@ def attn_params(**kw):
     (UNSUPPORTED, dict(impl=kdv.KDV_IMPL_TC, scale=0.0)), (UNSUPPORTED, dict(num_splits=5000)),
     (INVALID, dict(q=None)), (INVALID, dict(c8=None)), (INVALID, dict(kr=None)), (INVALID, dict(kv_scale=None)), (INVALID, dict(kv_off=None)),
     (INVALID, dict(tree_off=None)), (INVALID, dict(o=None)), (INVALID, dict(q=P + 1)), (INVALID, dict(mask=P + 4)), (INVALID, dict(num_slots=-1)),
-    (WORKSPACE, dict(num_splits=2)), (WORKSPACE, dict(num_splits=2, workspace=P, workspace_bytes=100)),
+    (INVALID, dict(impl=kdv.KDV_IMPL_TC, q=P + 8)), (INVALID, dict(impl=kdv.KDV_IMPL_TC, q_row_stride=577)), (INVALID, dict(impl=kdv.KDV_IMPL_TC, c8=P + 8)),
+    (INVALID, dict(impl=kdv.KDV_IMPL_TC, kr=P + 2)), (INVALID, dict(impl=kdv.KDV_IMPL_TC, o=P + 4)), (WORKSPACE, dict(num_splits=2)), (WORKSPACE, dict(num_splits=2, workspace=P, workspace_bytes=100)),
 ])
 def test_attn_refusals(want, kw):
     assert status("kdv_verify_attn8", attn_params(**kw)) == want
