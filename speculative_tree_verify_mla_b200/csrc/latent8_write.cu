@@ -10,7 +10,7 @@
 // row counts launch latency. One warp takes a row: each lane holds 16 latent
 // elements in registers between the maximum and the rounding (one read), and
 // one rope pair, whose angle it forms itself; everything a row needs from memory is asked
-// for at once, the next row's slot and position before that. A scale that is a power of two divides as a product (exact). 65536 bf16 rows: 31 us
+// for at once, the next row's slot and position before that. A scale that is a power of two divides as a product (exact). 65536 bf16 rows: 30 us
 // (49 us with a division for each element and the position read last).
 #include <cuda_fp8.h>
 
@@ -45,11 +45,10 @@ struct WriteArgs {
   float mscale;
 };
 
-// The least e with x <= 448 * 2^e = 0.875 * 2^(e + 9), clamped below at -100.
-__device__ inline int scale_exponent(float amax) {
-  int e;
-  const float m = frexpf(amax, &e);                 // amax = m 2^e, m in [1/2, 1)
-  return max(m <= 0.875f ? e - 9 : e - 8, -100);
+// The least e >= -100 with x <= 448 * 2^e = 1.75 * 2^(e + 8), from x's bits (x > 0, finite; what is too
+// small to be normal is below every e that counts).
+__device__ inline int scale_exponent(uint32_t bits) {
+  return max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100);
 }
 
 __device__ inline bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
@@ -114,6 +113,23 @@ struct RowIn {
     }
     slot = find_slot(a, i);
   }
+  // the largest magnitude of this lane's elements, as the bits of a float
+  __device__ __forceinline__ uint32_t magnitude() const {
+    uint32_t m = 0;
+    if constexpr (!FAST) {
+#pragma unroll
+      for (int j = 0; j < PER_LANE; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
+      return m;
+    } else {
+#pragma unroll
+      for (int g = 0; g < WORDS; ++g) {
+        const uint32_t u[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = sizeof(T) == 2 ? __vmaxu2(m, u[j] & 0x7fff7fffu) : max(m, u[j] & 0x7fffffffu);
+      }
+      return sizeof(T) == 2 ? max(m & 0xffff0000u, m << 16) : m;
+    }
+  }
   __device__ __forceinline__ void get(float (&v)[PER_LANE]) const {
     if constexpr (!FAST) {
 #pragma unroll
@@ -146,21 +162,18 @@ __device__ __forceinline__ void write_row(const WriteArgs& a, int i, const RowIn
   const int first = a.half ? lane : 2 * lane, second = a.half ? lane + npair : 2 * lane + 1;
   const float ku = (float)in.ku, kv = (float)in.kv;
 
-  float amax = 0.f;
-#pragma unroll
-  for (int j = 0; j < PER_LANE; ++j) amax = fmaxf(amax, fabsf(v[j]));
-  bool bad = !finite(amax);
-#pragma unroll
-  for (int j = 0; j < PER_LANE; ++j) bad |= isnan(v[j]);
-  bad = __any_sync(0xffffffffu, bad);              // the row has values that are not finite: left out of amax, stored as NaN
-  if (bad) {
+  // magnitudes order as their bits do, infinities and NaN above all
+  uint32_t top = __reduce_max_sync(0xffffffffu, in.magnitude());
+  if (top >= 0x7f800000u) {                        // left out of the maximum, stored as NaN
     if (lane == 0) record_error(a.d_err, KDV_DERR_RANGE);
-    amax = 0.f;
+    top = 0;
 #pragma unroll
     for (int j = 0; j < PER_LANE; ++j) {
-      amax = fmaxf(amax, finite(v[j]) ? fabsf(v[j]) : 0.f);
-      v[j] = finite(v[j]) ? v[j] : __int_as_float(0x7fc00000);
+      const bool ok = finite(v[j]);
+      top = max(top, ok ? __float_as_uint(fabsf(v[j])) : 0u);
+      v[j] = ok ? v[j] : __int_as_float(0x7fc00000);
     }
+    top = __reduce_max_sync(0xffffffffu, top);
   }
   if (a.static_scale) {
     if (!(s > 0.f) || !finite(s)) {
@@ -168,9 +181,7 @@ __device__ __forceinline__ void write_row(const WriteArgs& a, int i, const RowIn
       return;
     }
   } else {
-    // magnitudes order as their bits do
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-    s = amax == 0.f ? 1.f : ldexpf(1.f, scale_exponent(amax));
+    s = top == 0u ? 1.f : __int_as_float((127 + scale_exponent(top)) << 23);
     if (lane == 0) a.scale[slot] = s;
   }
   // 2^-e of s = 2^e, for every e whose inverse is a normal number

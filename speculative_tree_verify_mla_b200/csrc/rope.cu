@@ -9,7 +9,7 @@
 // 64-bit angles are what a per-element version would spend its time on: a
 // head count of 64 would repeat each one 64 times), while the first vectors
 // are on their way, then streams the vectors through registers, four 16-byte units in flight a
-// thread. 8192 tokens x 64 heads x 128 dims, half of them rotated: 57 us (86 us with
+// thread. 8192 tokens x 64 heads x 128 dims, half of them rotated: 49 us (86 us with
 // the loads behind the table and a division for each unit).
 #include <algorithm>
 #include <cmath>
@@ -37,6 +37,12 @@ struct RopeArgs {
 template <typename T, int V> struct Vec;
 template <> struct Vec<__nv_bfloat16, 8> {
   uint4 w;
+  __device__ Vec from_lane(int lane) const {
+    Vec r;
+    r.w = make_uint4(__shfl_sync(0xffffffffu, w.x, lane), __shfl_sync(0xffffffffu, w.y, lane), __shfl_sync(0xffffffffu, w.z, lane),
+                     __shfl_sync(0xffffffffu, w.w, lane));
+    return r;
+  }
   __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
   __device__ void get(float (&f)[8]) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -58,6 +64,14 @@ template <> struct Vec<__nv_bfloat16, 8> {
 };
 template <> struct Vec<float, 8> {
   float4 a, b;
+  __device__ Vec from_lane(int lane) const {
+    Vec r;
+    r.a = make_float4(__shfl_sync(0xffffffffu, a.x, lane), __shfl_sync(0xffffffffu, a.y, lane), __shfl_sync(0xffffffffu, a.z, lane),
+                      __shfl_sync(0xffffffffu, a.w, lane));
+    r.b = make_float4(__shfl_sync(0xffffffffu, b.x, lane), __shfl_sync(0xffffffffu, b.y, lane), __shfl_sync(0xffffffffu, b.z, lane),
+                      __shfl_sync(0xffffffffu, b.w, lane));
+    return r;
+  }
   __device__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -78,15 +92,32 @@ template <typename T> struct Vec<T, 1> {
   __device__ static void store(T* p, const float (&f)[1]) { *p = (T)f[0]; }
 };
 
+template <int N> __device__ __forceinline__ void read_pairs(float2 (&out)[N], const float2* at) {
+  if constexpr (N == 1) {
+    out[0] = *at;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float4 w = reinterpret_cast<const float4*>(at)[i];
+      out[2 * i] = make_float2(w.x, w.y);
+      out[2 * i + 1] = make_float2(w.z, w.w);
+    }
+  }
+}
+
 // A unit is V elements (both members of its pairs): with V = 8 four
-// interleaved pairs, or eight of the first half with their eight partners
-// (two Vecs); with V = 1 one pair as two scalars. Units behind the rotated
-// part copy V elements.
-template <typename TX, typename TY, int V, bool HALF>
+// interleaved pairs (NEIGHBOURS), or eight of the first half with their eight partners
+// (HALVES: two Vecs); with V = 1 one pair as two scalars. Units behind the rotated
+// part copy V elements. HALVES_BY_LANES: every unit is eight elements where they lie and the partner's
+// come from another lane, so that a warp's accesses are whole lines (two Vecs a thread leave gaps:
+// 49 us instead of 57); it takes partners that are a power of two of units apart, and vectors of whole such groups.
+enum { NEIGHBOURS, HALVES, HALVES_BY_LANES };
+template <typename TX, typename TY, int V, int PAIRING>
 __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ RopeArgs a,
                                                        const __grid_constant__ RopeTurns<KDV_MAX_ROT / 2> turns) {
-  __shared__ float2 table[TABLE];
-  constexpr bool TWO = HALF || V == 1;                  // the pair's members are in two Vecs
+  __shared__ __align__(16) float2 table[TABLE];
+  constexpr bool HALF = PAIRING != NEIGHBOURS, LANES = PAIRING == HALVES_BY_LANES;
+  constexpr bool TWO = (HALF && !LANES) || V == 1;      // the pair's members are in two Vecs of a thread
   const int pairs = a.rot / 2;
   const int t0 = blockIdx.x * a.group;
   const int nt = min(a.group, a.tokens - t0);
@@ -110,7 +141,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
         int e, second = 0;                              // the unit's element, and its partner's distance
         if (un >= rot_units) {
           e = a.rot + (un - rot_units) * V;
-        } else if (HALF) {
+        } else if (HALF && !LANES) {
           e = un * V;
           second = pairs;
         } else if (V == 1) {
@@ -121,7 +152,7 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
         }
         const int64_t xo = (int64_t)(t0 + t) * a.xt + (int64_t)(h0 + h) * a.xh + e;
         yo[n] = (int64_t)(t0 + t) * a.yt + (int64_t)(h0 + h) * a.yh + e;
-        cs_at[n] = un < rot_units ? t * pairs + un * (TWO ? V : V / 2) : -1;
+        cs_at[n] = un < rot_units ? t * pairs + (LANES ? un * V & (pairs - 1) : un * (TWO ? V : V / 2)) : -1;
         u[n].load(x + xo);
         if (TWO && un < rot_units) v[n].load(x + xo + second);
       }
@@ -135,16 +166,36 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
     table[i] = cs;
   }
   __syncthreads();
-  for (int base = threadIdx.x; base < total; base += THREADS * INFLIGHT) {
+  for (int base = threadIdx.x; base - (int)(threadIdx.x & 31) < total; base += THREADS * INFLIGHT) {
     if (base != (int)threadIdx.x) load(base);
 #pragma unroll
     for (int n = 0; n < INFLIGHT; ++n) {
       const int i = base + n * THREADS;
+      if constexpr (LANES) {
+        // the partner's elements are `apart` lanes away; its lane is in range where this one is
+        const int apart = pairs / V;
+        v[n] = u[n].from_lane((threadIdx.x & 31) ^ apart);
+        if (i < total) {
+          float f[V], g[V];
+          u[n].get(f);
+          if (cs_at[n] >= 0) {
+            float2 cs[V];
+            read_pairs(cs, table + cs_at[n]);
+            const float side = i & apart ? 1.f : -1.f;  // second halves add u sin, first ones take v sin away
+            v[n].get(g);
+#pragma unroll
+            for (int k = 0; k < V; ++k) f[k] = f[k] * cs[k].x + side * cs[k].y * g[k];
+          }
+          Vec<TY, V>::store(y + yo[n], f);
+        }
+        continue;
+      }
       if (i < total) {
         float f[V], g[V];
         u[n].get(f);
         if (cs_at[n] >= 0) {
-          const float2* cs = table + cs_at[n];
+          float2 cs[TWO || LANES ? V : V / 2];                   // (in 16-byte pieces: a unit's entries begin at one)
+          read_pairs(cs, table + cs_at[n]);
           if constexpr (TWO) {
             v[n].get(g);
 #pragma unroll
@@ -172,13 +223,14 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const __grid_constant__ R
 }
 
 template <typename TX, typename TY>
-void launch_typed(const RopeArgs& a, const RopeTurns<KDV_MAX_ROT / 2>& f, bool half, bool vec, dim3 grid, cudaStream_t s) {
+void launch_typed(const RopeArgs& a, const RopeTurns<KDV_MAX_ROT / 2>& f, bool half, bool vec, bool lanes, dim3 grid, cudaStream_t s) {
   if (vec) {
-    if (half) rope_kernel<TX, TY, 8, true><<<grid, THREADS, 0, s>>>(a, f);
-    else rope_kernel<TX, TY, 8, false><<<grid, THREADS, 0, s>>>(a, f);
+    if (lanes) rope_kernel<TX, TY, 8, HALVES_BY_LANES><<<grid, THREADS, 0, s>>>(a, f);
+    else if (half) rope_kernel<TX, TY, 8, HALVES><<<grid, THREADS, 0, s>>>(a, f);
+    else rope_kernel<TX, TY, 8, NEIGHBOURS><<<grid, THREADS, 0, s>>>(a, f);
   } else {
-    if (half) rope_kernel<TX, TY, 1, true><<<grid, THREADS, 0, s>>>(a, f);
-    else rope_kernel<TX, TY, 1, false><<<grid, THREADS, 0, s>>>(a, f);
+    if (half) rope_kernel<TX, TY, 1, HALVES><<<grid, THREADS, 0, s>>>(a, f);
+    else rope_kernel<TX, TY, 1, NEIGHBOURS><<<grid, THREADS, 0, s>>>(a, f);
   }
 }
 
@@ -277,9 +329,11 @@ kdv_status kdv_rope(const kdv_rope_params* p, void* stream) {
   const bool vec = p->rot_dim % (half ? 16 : 8) == 0 && p->dim % 8 == 0 && rows16(p->x, a.xt, a.xh, xe) &&
                    rows16(p->y, a.yt, a.yh, ye);
   // One pass of the CTA's threads (INFLIGHT units each) is its share: whole
-  // tokens while their vectors are few, else a range of one token's heads.
-  const int V = vec ? 8 : 1, pairs = p->rot_dim / 2;
-  const int64_t units = ((half || V == 1) ? pairs / V : p->rot_dim / V) + (p->dim - p->rot_dim) / V;
+  // tokens while their vectors are few, else a range of one token's heads. (Four passes a CTA
+  // measured 65 us where one takes 57: CTAs that wait for their angles cover one another.)
+  const int V = vec ? 8 : 1, pairs = p->rot_dim / 2, apart = pairs / 8;
+  const bool lanes = vec && half && (apart & (apart - 1)) == 0 && apart <= 16 && p->dim / 8 % (2 * apart) == 0;
+  const int64_t units = (((half && !lanes) || V == 1) ? pairs / V : p->rot_dim / V) + (p->dim - p->rot_dim) / V;
   const int64_t share = THREADS * INFLIGHT;
   a.heads_per_cta = (int)std::max<int64_t>(1, std::min<int64_t>(p->heads, share / std::max<int64_t>(1, units)));
   a.group = a.heads_per_cta < p->heads
@@ -291,10 +345,10 @@ kdv_status kdv_rope(const kdv_rope_params* p, void* stream) {
   if (gy > 65535 || units * a.heads_per_cta * a.group > INT32_MAX / 2) return KDV_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)gx, (unsigned)gy);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (xe == 2 && ye == 2) launch_typed<__nv_bfloat16, __nv_bfloat16>(a, f, half, vec, grid, s);
-  else if (xe == 2) launch_typed<__nv_bfloat16, float>(a, f, half, vec, grid, s);
-  else if (ye == 2) launch_typed<float, __nv_bfloat16>(a, f, half, vec, grid, s);
-  else launch_typed<float, float>(a, f, half, vec, grid, s);
+  if (xe == 2 && ye == 2) launch_typed<__nv_bfloat16, __nv_bfloat16>(a, f, half, vec, lanes, grid, s);
+  else if (xe == 2) launch_typed<__nv_bfloat16, float>(a, f, half, vec, lanes, grid, s);
+  else if (ye == 2) launch_typed<float, __nv_bfloat16>(a, f, half, vec, lanes, grid, s);
+  else launch_typed<float, float>(a, f, half, vec, lanes, grid, s);
   return cudaGetLastError() == cudaSuccess ? KDV_OK : KDV_ERR_CUDA;
 }
 

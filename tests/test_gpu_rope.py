@@ -52,6 +52,15 @@ def test_shapes(n, heads, dim, rot, gap, half):
     assert torch.all(y[:, :, :gap] == 7.0)                  # nothing outside the head vectors
 
 
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("n,heads,dim,rot", [(19, 5, 128, 64), (3, 3, 192, 64), (2, 1, 64, 32), (1, 3, 64, 16), (70, 9, 256, 256), (11, 2, 192, 128), (5, 1, 96, 48)])
+def test_halves_at_all_distances(n, heads, dim, rot, xt, yt):
+    """Partners 1 to 16 units of eight elements away, and distances and widths that do not divide."""
+    x, pos, freq, y, p = make(n, heads, dim, rot, 1, n + rot, xt, yt)
+    kdv.kdv_rope(p)
+    check(x, pos, freq, y, rot, 1)
+
+
 @pytest.mark.parametrize("xt,yt", [("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
 @pytest.mark.parametrize("half", [0, 1])
 def test_types_and_far_positions(xt, yt, half):
