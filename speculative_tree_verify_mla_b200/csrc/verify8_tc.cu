@@ -30,7 +30,7 @@
 // One CTA per work item: 64 query rows of one request, one key split, tiles
 // of 96 keys. (The queries take 80 KB of shared memory. Beside them two tiles of 96
 // fit, so that the softmax of one runs during P.V of the one before and Q.K^T of the one behind; two
-// of 128 do not, and 16 nodes over 200k keys took 502 us instead of 468. The MMAs' rows 96-127 are
+// of 128 do not: 7 % slower over 200k keys. The MMAs' rows 96-127 are
 // whatever follows a block; nothing reads what they give.)
 //   warps 17-19 producers: gather 128-byte row pieces through the page table
 //               with cp.async into a ring of ten 12 KB blocks (two rope blocks,
@@ -45,8 +45,9 @@
 //
 // What bounds it: the tensor core and shared memory. A tile's 16 (N = 128) + 4 + 36 (N = 64) MMAs take
 // 2.55k clocks alone and 3.3k beside the copies and the softmax; one cp.async block of 12 KB takes
-// ~400. Over 200k keys the part runs into its power cap: 468 us in bursts, 537 us sustained (16
-// nodes x 64 heads, 952 and 830 TFLOP/s of the logical products). Few rows over short contexts: 16k clocks an item
+// ~400. Over 200k keys the part runs into its power cap: 466 us in bursts, 545 us sustained (16
+// nodes x 64 heads, 956 and 818 TFLOP/s of the logical products). Contiguous pools through TMA
+// boxes instead of the gather: 486 and 556 us, so there is one way to bring keys in. Few rows over short contexts: 16k clocks an item
 // for set-up, queries, first tile and output, and the merge (4-7 us).
 #include <cuda_fp8.h>
 
@@ -543,11 +544,11 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 
     // This key's scale is read a tile ahead, its slot two. The ring holds little more
     // than a tile, so a block's copies start late: its rows are asked into L2 when their
-    // slots are known, a 128-byte line by each group (and not by the copying warps, where the
-    // requests of random rows back up: 900 to 2200 clocks a tile).
+    // slots are known, a 128-byte line by each group, for all row tiles of a request by the
+    // first one (measured over 200k keys: 466 us, 479 with every row tile's own requests, 488 with none).
     auto scale_of = [&](int slot) { return slot < 0 ? 0.f : a.kv_scale[slot >> a.block_log2]; };
     auto prefetch = [&](int slot) {
-      if (slot < 0) return;
+      if (slot < 0 || rt != 0) return;
       prefetch_l2(a.c8 + (int64_t)slot * DC + 128 * g);
       if (g == 0) prefetch_l2(static_cast<const __nv_bfloat16*>(a.kr) + (int64_t)slot * DR);
     };

@@ -138,6 +138,34 @@ def test_unseen_keys_never_reach_an_output(impl):
         assert torch.isnan(r.o[own]).any(1).all() and torch.isnan(r.lse[own]).all(), what
 
 
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+@pytest.mark.parametrize("what", ["codes", "rope_nan", "rope_inf", "scale_nan", "scale_inf"])
+def test_neighbours_in_a_contiguous_pool_never_reach_an_output(impl, what):
+    """A tile behind a request's last key holds the next request's rows: whatever they are, the first one keeps its bits."""
+    c = plain8.Attn(30, [100, 40, 5], [tree(3), tree(2), tree(1)], 64, paged=False)
+    clean = Run(c, impl).go().check()
+    lo, hi = int(c.kv_off[1]), int(c.kv_off[2])
+    if what == "codes":
+        c.c8[lo:hi] = 0x7F
+    elif what.startswith("rope"):
+        c.kr[lo:hi] = float("nan") if what == "rope_nan" else float("inf")
+    else:
+        c.scale[lo:hi] = np.nan if what == "scale_nan" else np.inf
+    r = Run(c, impl).go()
+    rest = np.setdiff1d(np.arange(6 * 64), np.arange(3 * 64, 5 * 64))
+    assert torch.equal(r.o[rest], clean.o[rest]) and torch.equal(r.lse[rest], clean.lse[rest])
+    assert torch.isnan(r.lse[3 * 64:5 * 64]).all()
+
+
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+def test_contiguous_keys_beyond_the_pool(impl):
+    """Keys of a contiguous request that lie behind the pool's end are left out and reported."""
+    c = plain8.Attn(31, [250], [tree(2)], 64, paged=False)
+    Run(c, impl, num_slots=200).go().check(err=kdv.KDV_DERR_BAD_SLOT, drop=np.arange(200, 252))
+    r = Run(c, impl, num_slots=0).go()
+    assert r.err.item() == kdv.KDV_DERR_BAD_SLOT and torch.all(r.o == 0) and torch.all(torch.isneginf(r.lse))
+
+
 def test_query_that_is_not_finite_stays_in_its_row():
     c = plain8.Attn(9, [200], [tree(3)], 64)
     clean = Run(c).go().check()
@@ -326,8 +354,8 @@ def test_many_short_requests():
 
 def test_a_wait_that_runs_out_is_reported():
     """Waits limited to 1 ns end the call with an error; the next call is right. The same without splits."""
-    c = plain8.Attn(25, [3000], [tree(4)], 64)
-    for splits in (0, 1):
+    for splits, paged in ((0, True), (1, True), (0, False), (1, False)):
+        c = plain8.Attn(25, [3000], [tree(4)], 64, paged=paged)
         good = Run(c, TC, splits=splits).go().check()
         r = Run(c, TC, splits=splits, wait_limit_ns=1).go()
         torch.cuda.synchronize()
