@@ -160,7 +160,6 @@ __global__ void __launch_bounds__(WARPS * 32) verify8_simt_kernel(const __grid_c
 // row, a thread holds four neighbouring dims and reads eight parts at a time;
 // the parts' weights are formed once, 128 of them at a time, in shared memory.
 constexpr int MERGE_THREADS = 128;
-template <typename TP>
 __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_constant__ Verify8Args a,
                                                                  const __grid_constant__ VerifyPlan p) {
   __shared__ float weight[MERGE_THREADS];
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
   m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
   if (m == INFINITY) m = __int_as_float(0x7fc00000);
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  const TP* part = static_cast<const TP*>(a.part_o);
+  const float* part = static_cast<const float*>(a.part_o);
   const int d0 = 4 * tid;                                  // D_c <= 512
   const bool whole = D % 4 == 0;
   for (int k0 = 0; k0 < S; k0 += MERGE_THREADS) {
@@ -201,7 +200,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
     }
     __syncthreads();
     if (d0 >= D) continue;
-    const TP* src = part + (base + (int64_t)k0 * rows_b) * D + d0;
+    const float* src = part + (base + (int64_t)k0 * rows_b) * D + d0;
     const int64_t step = (int64_t)rows_b * D;
     for (int k = 0; k < n; k += 8) {
       float v[8][4];
@@ -211,15 +210,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
         for (int i = 0; i < 4; ++i) v[j][i] = 0.f;
         if (k + j >= n) continue;
         if (whole) {
-          if constexpr (sizeof(TP) == 2) {
-            const uint2 w = *reinterpret_cast<const uint2*>(src + j * step);
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-            v[j][0] = x.x; v[j][1] = x.y; v[j][2] = y.x; v[j][3] = y.y;
-          } else {
-            const float4 w = *reinterpret_cast<const float4*>(src + j * step);
-            v[j][0] = w.x; v[j][1] = w.y; v[j][2] = w.z; v[j][3] = w.w;
-          }
+          const float4 w = *reinterpret_cast<const float4*>(src + j * step);
+          v[j][0] = w.x; v[j][1] = w.y; v[j][2] = w.z; v[j][3] = w.w;
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) if (d0 + i < D) v[j][i] = (float)src[j * step + i];
@@ -264,6 +256,99 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
   }
 }
 
+// The same for the tensor-core kernel's parts (fp16, 512 dims): one warp a row, no barrier;
+// the first four parts are on their way before their weights are known. 5.5k layer (832 rows, 10
+// parts): 30.0 us in all, 30.4 with a CTA a row as above; 32 ragged single tokens 72 and 76 us.
+constexpr int ROW_WARPS = 4;
+__global__ void __launch_bounds__(ROW_WARPS * 32) combine8_rows_kernel(const __grid_constant__ Verify8Args a,
+                                                                       const __grid_constant__ VerifyPlan p) {
+  constexpr int AHEAD = 4;
+  const int lane = threadIdx.x & 31, row = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.launch_dependents;");       // the next launch may prepare itself
+  if (row >= p.total_rows) return;
+  int b = 0;
+  while (b + 1 < p.B && p.tree_base[b + 1] * p.H <= row) ++b;
+  const int rows_b = p.T[b] * p.H, S = p.S[b];
+  const int64_t base = (int64_t)p.part_base[b] + row - p.tree_base[b] * p.H;
+  const uint4* part = static_cast<const uint4*>(a.part_o) + base * 64 + lane;      // 64 pieces a row: lane and 32 + lane
+  const int64_t step = (int64_t)rows_b * 64;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the attention kernel's parts
+  uint4 x[AHEAD][2];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j)
+      if (k0 + j < S) {
+        x[j][0] = part[(k0 + j) * step];
+        x[j][1] = part[(k0 + j) * step + 32];
+      }
+  };
+  load(0);
+  float m = -INFINITY;
+  bool bad = false;                                        // a NaN part makes the row NaN
+  float2 su = make_float2(-INFINITY, 0.f);                 // of part `lane`
+  for (int k = lane; k < S; k += 32) {
+    const float2 v = a.part_s[base + (int64_t)k * rows_b];
+    if (k == lane) su = v;
+    bad |= isnan(v.x);
+    m = fmaxf(m, v.x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (__any_sync(0xffffffffu, bad)) m = __int_as_float(0x7fc00000);
+  float acc[16], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int k0 = 0; k0 < S; k0 += 32) {                     // 32 parts' weights at a time, one a lane
+    if (k0 > 0) su = k0 + lane < S ? a.part_s[base + (int64_t)(k0 + lane) * rows_b] : make_float2(-INFINITY, 0.f);
+    const float e = su.x == -INFINITY ? 0.f : expf(su.x - m);
+    const float weight = e * su.y;
+    sum += e;
+    const int n = min(32, S - k0);
+    for (int k = 0; k < n; k += AHEAD) {
+      if (k0 + k > 0) load(k0 + k);
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const float w = __shfl_sync(0xffffffffu, weight, (k + j) & 31);
+        if (k + j >= n) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t u[4] = {x[j][h].x, x[j][h].y, x[j][h].z, x[j][h].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+            acc[8 * h + 2 * i] = fmaf(w, f.x, acc[8 * h + 2 * i]);
+            acc[8 * h + 2 * i + 1] = fmaf(w, f.y, acc[8 * h + 2 * i + 1]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const bool none = m == -INFINITY;
+  const float inv = none ? 0.f : 1.f / sum;
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m + logf(sum);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = none ? 0.f : acc[i] * inv;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* v = acc + 8 * h;
+    const int64_t at = (int64_t)row * 64 + 32 * h + lane;  // in pieces of eight dims; o is 16-byte aligned here
+    if (a.out_f32) {
+      static_cast<float4*>(a.o)[2 * at] = make_float4(v[0], v[1], v[2], v[3]);
+      static_cast<float4*>(a.o)[2 * at + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t*>(&y);
+      }
+      static_cast<uint4*>(a.o)[at] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_verify8_simt(const Verify8Args& a, const VerifyPlan& p, cudaStream_t stream) {
@@ -280,16 +365,15 @@ cudaError_t launch_combine8(const Verify8Args& a, const VerifyPlan& p, cudaStrea
   // a programmatic dependent of the attention kernel: its launch overlaps that
   // kernel's end, its reads wait for it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.total_rows);
-  cfg.blockDim = dim3(MERGE_THREADS);
+  cfg.gridDim = dim3((unsigned)(p.part_f16 ? (p.total_rows + ROW_WARPS - 1) / ROW_WARPS : p.total_rows));
+  cfg.blockDim = dim3(p.part_f16 ? ROW_WARPS * 32 : MERGE_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return p.part_f16 ? cudaLaunchKernelEx(&cfg, combine8_kernel<__half>, a, p)
-                    : cudaLaunchKernelEx(&cfg, combine8_kernel<float>, a, p);
+  return cudaLaunchKernelEx(&cfg, p.part_f16 ? combine8_rows_kernel : combine8_kernel, a, p);
 }
 
 }  // namespace kdv
