@@ -229,7 +229,15 @@ struct QueryRow {
     u[4] = w1.x; u[5] = w1.y; u[6] = w1.z; u[7] = w1.w;
   }
   // Writes the row's terms; returns its logit factor scale log2(e) 2^-k.
-  __device__ __forceinline__ float stage(float scale, int r, uint8_t* sp, int lane) const {
+  __device__ __forceinline__ float stage(float scale, int r, bool valid, uint8_t* sp, int lane) const {
+    const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
+    *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
+    if (!valid) {
+      *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = 0u;
+      return 1.f;
+    }
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
@@ -270,12 +278,10 @@ struct QueryRow {
         lo[i] = j == 0 ? l : lo[i] | (l << 16);
       }
     }
-    const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     const float ra = __uint_as_float(rope << 16) * up, rb = __uint_as_float(rope & 0xffff0000u) * up;
     *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = pack_bf16x2(ra, rb);
-    *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
     return fminf(fmaxf(scale * LOG2E * __int_as_float((127 - e) << 23), 1.17549435e-38f), 3.402823466e38f);
   }
 };
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 4 * warp + k;
-        const float c = row[k].stage(a.scale, r, sp, lane);
+        const float c = row[k].stage(a.scale, r, r0 + r < rows_b, sp, lane);
         if (lane == 0) {
           float* f = reinterpret_cast<float*>(sp + OFF_CM) + (r / 2) * 4 + (r & 1);
           f[0] = c;
