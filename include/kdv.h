@@ -626,7 +626,7 @@ typedef struct kdv_logits_params {
   int32_t batch;           /* B in [1, KDV_MAX_BATCH]                            */
   int32_t max_T;           /* [1, 64]: bound on every T_b                        */
   int32_t total_nodes;     /* sumT (HOST value; rows of logits and out)          */
-  int32_t vocab;           /* V >= 1                                             */
+  int32_t vocab;           /* V >= 1 (up to 65535 * 2048)                        */
   int32_t dtype;           /* KDV_BF16 / KDV_F32                                 */
   int32_t out_dtype;
   const void* logits;      /* [sumT][logits_ld]                                  */

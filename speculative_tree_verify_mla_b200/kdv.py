@@ -449,7 +449,7 @@ def _fill(p, kw: dict):
             p._keep.append(arr)
             setattr(p, k, ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32)))
         elif k == "h_inv_freq" and v is not None:
-            arr = np.array(v, dtype=np.float64)
+            arr = np.array(v.numpy() if isinstance(v, torch.Tensor) else v, dtype=np.float64)
             p._keep.append(arr)
             p.h_inv_freq = arr.ctypes.data
         elif isinstance(v, torch.Tensor):
