@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     float unit = 0.f, inv_unit = 0.f;                // the power of two that s_j is taken relative to
     const uint32_t quarter = tmem + ((uint32_t)(w * 32) << 16);
     const int key = w * 32 + lane;                   // also the dim of a block; the last quarter has no keys
-    const int no_key = key < KEYS ? 0 : 1 << 30;     // added to a key that there is not
+    auto key_of = [&](int tile) { return key < KEYS ? k_lo + tile * KEYS + key : k_hi; };   // k_hi: no key
     uint8_t* prow = sp + OFF_P + key * ROWS + (((uint32_t)g ^ (((uint32_t)key >> 1) & 3u)) << 4);   // 64-byte swizzle
 
     // This key's scale is read a tile ahead, its slot two. The ring holds little more
@@ -558,9 +558,9 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       prefetch_l2(a.c8 + (int64_t)slot * DC + 128 * g);
       if (g == 0) prefetch_l2(static_cast<const __nv_bfloat16*>(a.kr) + (int64_t)slot * DR);
     };
-    int slot = entry_of(k_lo + key + no_key), slot_next = entry_of(k_lo + KEYS + key + no_key), entry = entry_of(k_lo + 2 * KEYS + key + no_key);
-    slot = slot_of(k_lo + key + no_key, slot);
-    slot_next = slot_of(k_lo + KEYS + key + no_key, slot_next);
+    int slot = entry_of(key_of(0)), slot_next = entry_of(key_of(1)), entry = entry_of(key_of(2));
+    slot = slot_of(key_of(0), slot);
+    slot_next = slot_of(key_of(1), slot_next);
     float ks = scale_of(slot), ks_next = scale_of(slot_next);
     prefetch(slot_next);
 
@@ -711,10 +711,10 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       if (lane == 0) mbar_arrive(bar(B_P));
       slot = slot_next;
       ks = ks_next;
-      slot_next = slot_of(k_lo + (i + 2) * KEYS + key + no_key, entry);
+      slot_next = slot_of(key_of(i + 2), entry);
       ks_next = scale_of(slot_next);
       prefetch(slot_next);
-      entry = entry_of(k_lo + (i + 3) * KEYS + key + no_key);
+      entry = entry_of(key_of(i + 3));
     }
 
     if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");   // the merge's launch overlaps the rest

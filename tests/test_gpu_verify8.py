@@ -377,3 +377,22 @@ def test_calls_back_to_back_share_a_workspace():
             r.go()
     for r in runs:
         r.check()
+
+
+def test_millions_of_keys_through_shared_slots():
+    """A page table that names the same 1000 slots 3000 times over: every weight repeats, so o is theirs and lse grows by ln 3000."""
+    c = plain8.Attn(32, [1000], [[-1]], 16, masks=[0])
+    o, lse, ob, lb = c.answer()
+    many = 3000
+    table = i32(np.concatenate([np.tile(c.table[:1000], many), c.table[1000:]]))
+    n = 1000 * many
+    r = Run(c, page_table=table, kv_off=i32([0, n + 1]), prefix_len=i32([n]), h_prefix_len=[n])
+    size = kdv.kdv_verify_attn8_workspace(r.p)
+    r.ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    r.p.workspace, r.p.workspace_bytes = r.ws.data_ptr(), size
+    r.go()
+    assert r.err.item() == 0
+    # sums of 3e6 / 148 items' equal terms round in fp32: 2^-24 for each of at most 2^15 additions in a chain, 2^-9 in all
+    e = np.abs(r.o.double().cpu().numpy() - o)
+    assert np.all(e <= ob + 2.0 ** -9 * (np.abs(o) + ob) + 2.0 ** -24 * np.abs(o))
+    assert np.all(np.abs(r.lse.double().cpu().numpy() - (lse + np.log(many))) <= lb + 2.0 ** -9)
