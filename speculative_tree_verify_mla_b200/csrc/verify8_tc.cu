@@ -228,30 +228,27 @@ struct QueryRow {
     u[0] = w0.x; u[1] = w0.y; u[2] = w0.z; u[3] = w0.w;
     u[4] = w1.x; u[5] = w1.y; u[6] = w1.z; u[7] = w1.w;
   }
-  // Writes the row's terms; returns its logit factor scale log2(e) 2^-k.
-  __device__ __forceinline__ float stage(float scale, int r, bool valid, uint8_t* sp, int lane) const {
-    const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
-    *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
-    if (!valid) {
-      *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = 0u;
-      return 1.f;
-    }
+  // The row's largest magnitude, as the bits of a bf16: 0x7f80 or more where it holds an infinity or a NaN.
+  __device__ __forceinline__ uint32_t magnitude() const {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
-    uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-    const bool bad = top >= 0x7f80u;               // an infinity or a NaN in the row (warp-uniform)
-    if (bad) {
-      m = 0;
+    return __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+  }
+  // The same of its finite elements alone.
+  __device__ __forceinline__ uint32_t finite_magnitude() const {
+    uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t lo = u[i] & 0x7fffu, hi = (u[i] >> 16) & 0x7fffu;
-        m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
-      }
-      top = __reduce_max_sync(0xffffffffu, m);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = u[i] & 0x7fffu, hi = (u[i] >> 16) & 0x7fffu;
+      m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
     }
+    return __reduce_max_sync(0xffffffffu, m);
+  }
+  // Writes the row's terms; returns its logit factor scale log2(e) 2^-k. bad: some element is not finite.
+  template <bool bad> __device__ __forceinline__ float stage(float scale, uint32_t top, int r, uint8_t* sp, int lane) const {
+    const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
+    *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
     // the power of two that brings the largest element into [128, 256)
     const int e = top == 0u ? 0 : max(-120, min(60, 7 + 127 - (int)(top >> 7)));
     const float up = __int_as_float((e + 127) << 23);
@@ -367,26 +364,23 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int local = item - p.item_base[b];
   const int split = local / p.tiles[b], rt = local - split * p.tiles[b];
-  const int L = p.L[b], n_keys = L + p.T[b], rows_b = p.T[b] * p.H;
+  const int rows_b = p.T[b] * p.H, r0 = rt * ROWS;
+  // this warp's query rows and a lane's row's mask: on their way while the CTA sets up
+  QueryRow row[4];
+  uint64_t qmask = 0;
+  if (warp < SOFTMAX_WARPS) {
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)p.tree_base[b] * p.H + r0 + 4 * warp) * a.q_row_stride;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) row[k].load(q + k * a.q_row_stride, r0 + 4 * warp + k < rows_b, lane);
+    const int lr = r0 + 4 * warp + lane;
+    if (lane < 4 && lr < rows_b) qmask = node_mask(a, p, b, lr / p.H);
+  }
+  const int L = p.L[b], n_keys = L + p.T[b];
   const bool ok = request_ok(a, p, b, tid == 0 && local == 0);
   const int64_t lo64 = (int64_t)split * p.chunk[b];
   const int k_lo = (int)min(lo64, (int64_t)n_keys);
   const int k_hi = ok ? (int)min(lo64 + p.chunk[b], (int64_t)n_keys) : k_lo;
   const int NT = (k_hi - k_lo + KEYS - 1) / KEYS;
-  const int r0 = rt * ROWS;
-
-  // this warp's query rows: on their way while the CTA sets up
-  QueryRow row[4];
-  uint64_t qmask[4] = {0, 0, 0, 0};
-  if (warp < SOFTMAX_WARPS) {
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int lr = r0 + 4 * warp + k;
-      row[k].load(q + ((int64_t)p.tree_base[b] * p.H + lr) * a.q_row_stride, lr < rows_b, lane);
-      if (lane == 0 && lr < rows_b) qmask[k] = node_mask(a, p, b, lr / p.H);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -522,16 +516,26 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     const uint32_t wg_bar = 1 + g;
     {
       // a warp stages four rows of its group, all loads in flight
+      float c[4] = {1.f, 1.f, 1.f, 1.f};
+      uint32_t top[4];
+      bool bad = false;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = 4 * warp + k;
-        const float c = row[k].stage(a.scale, r, r0 + r < rows_b, sp, lane);
-        if (lane == 0) {
-          float* f = reinterpret_cast<float*>(sp + OFF_CM) + (r / 2) * 4 + (r & 1);
-          f[0] = c;
-          f[2] = -NO_MAX;
-          reinterpret_cast<uint64_t*>(sp + OFF_MASK)[r] = qmask[k];
-        }
+      for (int k = 0; k < 4; ++k) top[k] = row[k].magnitude();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) bad |= top[k] >= 0x7f80u;          // (warp-uniform)
+      if (bad) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<true>(a.scale, row[k].finite_magnitude(), 4 * warp + k, sp, lane);
+      } else {                                       // four independent streams of instructions
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<false>(a.scale, top[k], 4 * warp + k, sp, lane);
+      }
+      if (lane < 4) {
+        const int r = 4 * warp + lane;
+        float* f = reinterpret_cast<float*>(sp + OFF_CM) + (r / 2) * 4 + (r & 1);
+        f[0] = lane == 0 ? c[0] : lane == 1 ? c[1] : lane == 2 ? c[2] : c[3];
+        f[2] = -NO_MAX;
+        reinterpret_cast<uint64_t*>(sp + OFF_MASK)[r] = qmask;
       }
     }
     fence_proxy_async_smem();
@@ -634,30 +638,25 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         const float smax = warp_max(isnan(s) ? 0.f : fabsf(s));
         if (lane == 0) red2[w] = smax;
         named_bar_sync(wg_bar, 128);
-        const int row = lane & (GROUP_ROWS - 1);
-        const float top = fmaxf(fmaxf(red[row], red[16 + row]), fmaxf(red[32 + row], red[48 + row]));   // NaN: no key moves it
+        if (w == 0) {                                // one warp moves the rows' references
+          const int row = lane & (GROUP_ROWS - 1);
+          const float top = fmaxf(fmaxf(red[row], red[16 + row]), fmaxf(red[32 + row], red[48 + row]));   // NaN: no key moves it
+          float* cr = reinterpret_cast<float*>(cm + row / 2) + (row & 1);
+          const float m_old = -cr[2], m_new = top - P_TOP > m_old ? top - P_TOP : m_old;
+          __syncwarp();
+          if (lane < GROUP_ROWS) {
+            cr[2] = -m_new;
+            fac[lane] = ex2(m_old - m_new);
+          }
+        }
+        // the scales' unit: the power of two at or above the largest, with room (2^-120 at least)
         const float st = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
-        float* cr = reinterpret_cast<float*>(cm + row / 2) + (row & 1);
-        const float m_old = -cr[2];
-        const float m_new = top - P_TOP > m_old ? top - P_TOP : m_old;
-        float unit_new = unit;
-        if (st > unit) {
-          int e;
-          const float m = frexpf(st, &e);
-          unit_new = UNIT_ROOM * ldexpf(1.f, max(m == 0.5f ? e - 1 : e, -120));
-        } else if (unit == 0.f) {
-          unit_new = ldexpf(1.f, -120);              // scales of 0 so far
-        }
-        const float shift = ex2(m_old - m_new);
-        named_bar_sync(wg_bar, 128);                 // all have read red, red2 and cm
-        if (w == 0 && lane < GROUP_ROWS) {
-          cr[2] = -m_new;
-          fac[lane] = shift;
-        }
-        named_bar_sync(wg_bar, 128);
-        const float us = unit / unit_new;
-        unit = unit_new;
+        const uint32_t pow2 = max((__float_as_uint(st) + 0x7fffffu) & 0xff800000u, (127u - 120u) << 23);
+        const float unit_new = st > unit || unit == 0.f ? UNIT_ROOM * __uint_as_float(pow2) : unit;
         inv_unit = 1.f / unit_new;
+        const float us = unit * inv_unit;
+        unit = unit_new;
+        named_bar_sync(wg_bar, 128);
         if (i > 0) {
           wait(bar(B_PV), (i - 1) & 1);              // P.V of the tiles before is complete
           tc_fence_after();
@@ -775,7 +774,9 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         for (int r = 0; r < 16; ++r) o[r] = ahead[r];
       }
     };
-    if (!direct) write(__half(), [](float v) { return __float2half_rn(v); }, a.part_o);
+    if (nr <= 0) {
+      // no rows of this group
+    } else if (!direct) write(__half(), [](float v) { return __float2half_rn(v); }, a.part_o);
     else if (a.out_f32) write(float(), [](float v) { return v; }, a.o);
     else write(__nv_bfloat16(), [](float v) { return __float2bfloat16_rn(v); }, a.o);
     tc_fence_before();
