@@ -256,48 +256,45 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
   }
 }
 
-// The same for the tensor-core kernel's parts (fp16, 512 dims): one warp a row, no barrier;
-// the first four parts are on their way before their weights are known. 5.5k layer (832 rows, 10
-// parts): 30.0 us in all, 30.4 with a CTA a row as above; 32 ragged single tokens 72 and 76 us.
+// The same for the tensor-core kernel's parts (fp16, 512 dims): one warp half a row, no barrier;
+// the first eight parts are on their way before their weights are known. 5.5k layer (832 rows, 10
+// parts): MERGE_A us in all, MERGE_B with a warp a row and four parts in flight, 30.4 against 30.0 with a CTA a row.
 constexpr int ROW_WARPS = 4;
 __global__ void __launch_bounds__(ROW_WARPS * 32) combine8_rows_kernel(const __grid_constant__ Verify8Args a,
                                                                        const __grid_constant__ VerifyPlan p) {
-  constexpr int AHEAD = 4;
-  const int lane = threadIdx.x & 31, row = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  constexpr int AHEAD = 8;
+  const int lane = threadIdx.x & 31, warp = blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
+  const int row = warp >> 1, piece = (warp & 1) * 32 + lane;               // eight of the row's dims
   asm volatile("griddepcontrol.launch_dependents;");       // the next launch may prepare itself
   if (row >= p.total_rows) return;
   int b = 0;
   while (b + 1 < p.B && p.tree_base[b + 1] * p.H <= row) ++b;
   const int rows_b = p.T[b] * p.H, S = p.S[b];
   const int64_t base = (int64_t)p.part_base[b] + row - p.tree_base[b] * p.H;
-  const uint4* part = static_cast<const uint4*>(a.part_o) + base * 64 + lane;      // 64 pieces a row: lane and 32 + lane
+  const uint4* part = static_cast<const uint4*>(a.part_o) + base * 64 + piece;
   const int64_t step = (int64_t)rows_b * 64;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the attention kernel's parts
-  uint4 x[AHEAD][2];
+  uint4 x[AHEAD];
   auto load = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j)
-      if (k0 + j < S) {
-        x[j][0] = part[(k0 + j) * step];
-        x[j][1] = part[(k0 + j) * step + 32];
-      }
+      if (k0 + j < S) x[j] = part[(k0 + j) * step];
   };
+  float2 su = lane < S ? a.part_s[base + (int64_t)lane * rows_b] : make_float2(-INFINITY, 0.f);   // of part `lane`
   load(0);
-  float m = -INFINITY;
-  bool bad = false;                                        // a NaN part makes the row NaN
-  float2 su = make_float2(-INFINITY, 0.f);                 // of part `lane`
-  for (int k = lane; k < S; k += 32) {
-    const float2 v = a.part_s[base + (int64_t)k * rows_b];
-    if (k == lane) su = v;
-    bad |= isnan(v.x);
-    m = fmaxf(m, v.x);
+  float m = su.x;
+  bool bad = isnan(su.x);                                  // a NaN part makes the row NaN
+  for (int k = lane + 32; k < S; k += 32) {
+    const float v = a.part_s[base + (int64_t)k * rows_b].x;
+    bad |= isnan(v);
+    m = fmaxf(m, v);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (__any_sync(0xffffffffu, bad)) m = __int_as_float(0x7fc00000);
-  float acc[16], sum = 0.f;
+  float acc[8], sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   for (int k0 = 0; k0 < S; k0 += 32) {                     // 32 parts' weights at a time, one a lane
     if (k0 > 0) su = k0 + lane < S ? a.part_s[base + (int64_t)(k0 + lane) * rows_b] : make_float2(-INFINITY, 0.f);
     const float e = su.x == -INFINITY ? 0.f : expf(su.x - m);
@@ -310,15 +307,12 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) combine8_rows_kernel(const __g
       for (int j = 0; j < AHEAD; ++j) {
         const float w = __shfl_sync(0xffffffffu, weight, (k + j) & 31);
         if (k + j >= n) break;
+        const uint32_t u[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t u[4] = {x[j][h].x, x[j][h].y, x[j][h].z, x[j][h].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            acc[8 * h + 2 * i] = fmaf(w, f.x, acc[8 * h + 2 * i]);
-            acc[8 * h + 2 * i + 1] = fmaf(w, f.y, acc[8 * h + 2 * i + 1]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+          acc[2 * i] = fmaf(w, f.x, acc[2 * i]);
+          acc[2 * i + 1] = fmaf(w, f.y, acc[2 * i + 1]);
         }
       }
     }
@@ -327,25 +321,21 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) combine8_rows_kernel(const __g
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const bool none = m == -INFINITY;
   const float inv = none ? 0.f : 1.f / sum;
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m + logf(sum);
+  if (piece == 0 && a.lse != nullptr) a.lse[row] = none ? -INFINITY : m + logf(sum);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = none ? 0.f : acc[i] * inv;
+  for (int i = 0; i < 8; ++i) acc[i] = none ? 0.f : acc[i] * inv;
+  const int64_t at = (int64_t)row * 64 + piece;            // o is 16-byte aligned here
+  if (a.out_f32) {
+    static_cast<float4*>(a.o)[2 * at] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    static_cast<float4*>(a.o)[2 * at + 1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  } else {
+    uint32_t u[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float* v = acc + 8 * h;
-    const int64_t at = (int64_t)row * 64 + 32 * h + lane;  // in pieces of eight dims; o is 16-byte aligned here
-    if (a.out_f32) {
-      static_cast<float4*>(a.o)[2 * at] = make_float4(v[0], v[1], v[2], v[3]);
-      static_cast<float4*>(a.o)[2 * at + 1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 y = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&y);
-      }
-      static_cast<uint4*>(a.o)[at] = make_uint4(u[0], u[1], u[2], u[3]);
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&y);
     }
+    static_cast<uint4*>(a.o)[at] = make_uint4(u[0], u[1], u[2], u[3]);
   }
 }
 
@@ -365,7 +355,7 @@ cudaError_t launch_combine8(const Verify8Args& a, const VerifyPlan& p, cudaStrea
   // a programmatic dependent of the attention kernel: its launch overlaps that
   // kernel's end, its reads wait for it
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.part_f16 ? (p.total_rows + ROW_WARPS - 1) / ROW_WARPS : p.total_rows));
+  cfg.gridDim = dim3((unsigned)(p.part_f16 ? (2 * p.total_rows + ROW_WARPS - 1) / ROW_WARPS : p.total_rows));
   cfg.blockDim = dim3(p.part_f16 ? ROW_WARPS * 32 : MERGE_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
