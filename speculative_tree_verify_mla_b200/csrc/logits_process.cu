@@ -15,7 +15,8 @@
 // each one in the tile has a number there, and a small matrix says how often
 // node t's path holds it, so the nodes need no barrier between them.
 // 13 nodes of 163840 tokens with 5553 of history: 9.5 us (38 with the tile's nodes one after
-// another and the path counted in and out around each); 160 nodes in fp32: 58 us (87).
+// another and the path counted in and out around each); 160 nodes in fp32: 49 us (87), the logits
+// read as streaming data, so that the results stay in L2 (53 otherwise).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -29,6 +30,7 @@ constexpr int THREADS = 256;
 constexpr int TOKENS = 8;                  // tokens a thread holds
 constexpr int TILE = THREADS * TOKENS;     // tokens a CTA holds
 constexpr int NODES = 2;                   // a CTA's nodes at least: one in hand, one on its way
+constexpr int L2_AHEAD = 3;                // nodes behind the one in hand whose logits are asked for into L2
 
 struct LogitsArgs {
   const void* x;
@@ -71,7 +73,7 @@ __device__ __forceinline__ float process(float x, uint32_t word, float bias, flo
 template <typename T, bool VEC> struct Row;
 template <> struct Row<__nv_bfloat16, true> {
   uint4 w;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w = *reinterpret_cast<const uint4*>(p + TOKENS * threadIdx.x); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int) { w = __ldcs(reinterpret_cast<const uint4*>(p + TOKENS * threadIdx.x)); }
   __device__ __forceinline__ float get(int j) const {
     const uint32_t u = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
     return __uint_as_float(j % 2 ? u & 0xffff0000u : u << 16);
@@ -80,8 +82,8 @@ template <> struct Row<__nv_bfloat16, true> {
 template <> struct Row<float, true> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p, int) {
-    a = reinterpret_cast<const float4*>(p + TOKENS * threadIdx.x)[0];
-    b = reinterpret_cast<const float4*>(p + TOKENS * threadIdx.x)[1];
+    a = __ldcs(reinterpret_cast<const float4*>(p + TOKENS * threadIdx.x));
+    b = __ldcs(reinterpret_cast<const float4*>(p + TOKENS * threadIdx.x) + 1);
   }
   __device__ __forceinline__ float get(int j) const {
     return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
@@ -162,6 +164,12 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
   uint32_t bits = 0xffu, bits_ahead = 0xffu;
   r.load(x + (int64_t)first * a.x_ld, n);
   bits = bits_of(allowed(first));
+
+  // The CTA's next rows come into L2 while it counts the history (160 nodes in fp32: 53 us, 59 without).
+  auto to_l2 = [&](int t) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(x + (int64_t)t * a.x_ld), "r"((uint32_t)(TILE * sizeof(TX))) : "memory");
+  };
+  if (VEC && tid > 0 && tid <= L2_AHEAD && first + tid < last) to_l2(first + tid);
 
   for (int i = tid; i < TILE / 4; i += THREADS) {
     reinterpret_cast<uint4*>(count)[i] = make_uint4(0, 0, 0, 0);
@@ -278,6 +286,7 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
     if (t + 1 < last) {
       ahead.load(x + (int64_t)(t + 1) * a.x_ld, n);
       bits_ahead = bits_of(allowed(t + 1));
+      if (VEC && tid == 0 && t + 1 + L2_AHEAD < last) to_l2(t + 1 + L2_AHEAD);
     }
     float f[TOKENS];
 #pragma unroll
