@@ -334,7 +334,10 @@ kdv_status kdv_rope(const kdv_rope_params* p, void* stream) {
   const int V = vec ? 8 : 1, pairs = p->rot_dim / 2, apart = pairs / 8;
   const bool lanes = vec && half && (apart & (apart - 1)) == 0 && apart <= 16 && p->dim / 8 % (2 * apart) == 0;
   const int64_t units = (((half && !lanes) || V == 1) ? pairs / V : p->rot_dim / V) + (p->dim - p->rot_dim) / V;
-  const int64_t share = THREADS * INFLIGHT;
+  // A CTA's units: one a thread until every SM has two CTAs, then up to as many as are in flight. 13 tokens x 64 heads
+  // x 64 dims: 2.4 us (3.2 in CTAs of four units a thread, of which there are 7); 416 tokens: 3.2 us (3.8).
+  const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(INFLIGHT, (int64_t)p->tokens * p->heads * units / (2 * 148 * THREADS)));
+  const int64_t share = THREADS * deep;
   a.heads_per_cta = (int)std::max<int64_t>(1, std::min<int64_t>(p->heads, share / std::max<int64_t>(1, units)));
   a.group = a.heads_per_cta < p->heads
                 ? 1
