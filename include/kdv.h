@@ -570,7 +570,8 @@ KDV_API kdv_status kdv_latent8_write(const kdv_latent8_params* p, void* stream);
  * than L + T has no keys (KDV_DERR_BAD_LENGTH).
  * The tensor-core kernel (KDV_IMPL_TC, AUTO's choice where it applies) takes
  * bf16 q, D_c = 512, D_r = 64, scale > 0, 16-byte aligned q, c8, kr, o and q rows;
- * KDV_IMPL_SIMT takes any D_c <= 512, D_r <= 64 and fp32 q.
+ * KDV_IMPL_SIMT takes any D_c <= 512, D_r <= 64 and fp32 q. TC resolves weights times scales down to 2^-24 of a
+ * row's largest; scales of 2^111 and more count as infinite there (NaN), those below 2^-108 lose precision.
  */
 typedef struct kdv_verify8_params {
   int32_t batch;           /* B in [1, KDV_MAX_BATCH]                            */

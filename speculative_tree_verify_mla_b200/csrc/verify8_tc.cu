@@ -13,11 +13,13 @@
 //   P.V    p s_j is rounded to fp16 and split in three e5m2 terms, the first
 //          two truncated (an e5m2 is an fp16's upper byte, so a term is a
 //          mask and the rest an exact subtraction), the last one rounded:
-//          2^-9 of p at most, against 2^-8 for a bf16 numerator. e5m2 reaches
-//          down to 2^-16 and the largest p is kept within [2^12, 2^15], so
-//          keys 2^-28 below the largest still count; with e4m3 terms a long
+//          2^-9 of p s at most, against 2^-8 for a bf16 numerator. e5m2 reaches
+//          down to 2^-16 and a row's largest p s is kept within [2^8, 2^15], so
+//          keys 2^-24 below the largest still count; with e4m3 terms a long
 //          tail of small weights would vanish (2^-18). Two terms would be
-//          off by 2.7e-3 (rms) at 0.85 of the time.
+//          off by 2.7e-3 (rms) at 0.85 of the time. The reference of a row's exponents
+//          is the largest log2(p s_j) of the keys that this row sees, not the largest logit:
+//          scales that differ widely, and those of keys that it does not see, take no precision from it.
 //
 // Both products are formed transposed, keys resp. latent dims as the rows (M)
 // of an MMA and 64 query rows as its columns (N): one token of 64 heads fills
@@ -40,8 +42,8 @@
 //   warp 16     MMA issue, one thread.
 //   warps 0-15  four warpgroups: queries in, softmax, output. Lane = key, so a
 //               warpgroup owns 16 query rows, a thread one key of them; a row's
-//               maximum is only looked for across lanes when some logit passes
-//               the reference by 2^3 (a vote), then O is rescaled in TMEM.
+//               maximum is only looked for across lanes when some p s passes
+//               the reference by 2^7 (a vote), then O is rescaled in TMEM.
 //
 // What bounds it: the tensor core and shared memory. A tile's 16 (N = 128) + 4 + 36 (N = 64) MMAs take
 // 2.55k clocks alone and 3.3k beside the copies and the softmax; one cp.async block of 12 KB takes
@@ -69,8 +71,13 @@ constexpr int GROUPS = 4, GROUP_ROWS = ROWS / GROUPS;       // softmax warpgroup
 constexpr int SOFTMAX_WARPS = 4 * GROUPS, MMA_WARP = SOFTMAX_WARPS, PRODUCER_WARPS = 3;
 constexpr int FIRST_PRODUCER = MMA_WARP + 1;
 constexpr int THREADS = (FIRST_PRODUCER + PRODUCER_WARPS) * 32;   // 640: 96 registers a thread
-constexpr float P_TOP = 12.f, P_GROW = 15.f; // log2 of the largest p when the reference is set / allowed later
-constexpr float UNIT_ROOM = 4.f;             // how far scales may grow before their unit moves
+// log2 of a row's largest numerator p s when its reference is set, and the most that it may grow to (5.5k layer: 26.2 us,
+// 27.0 with a reference set to 10, 28.9 with 12: references move less often)
+constexpr float P_TOP = 8.f, P_GROW = 15.f;
+// Scales are taken times 2^16: those of 2^-108 to 2^111 have room, smaller ones lose precision and larger ones count as infinite.
+constexpr float SCALE_UP = 65536.f, SCALE_UP_LOG2 = 16.f;
+constexpr float SCALE_MIN = -92.f;           // log2 of the least that a reference counts: p stays below 2^107, sums of 2^20 in fp32
+constexpr float PART_UNIT = 256.f;           // |o| <= 448 n 2^15 / l for n keys: 57344 in units of 256 n / l
 constexpr float NO_MAX = -1e30f;             // the reference of a row that has seen no key
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
@@ -86,8 +93,7 @@ constexpr int OFF_MASK = OFF_RING + RING * BLOCK;          // u64 [64] node mask
 constexpr int OFF_CM = OFF_MASK + ROWS * 8;                // float4 [32]: (c, c', -m, -m') of a row pair
 constexpr int OFF_RED = OFF_CM + 32 * 16;                  // float [GROUPS][4][16]
 constexpr int OFF_FAC = OFF_RED + GROUPS * 4 * GROUP_ROWS * 4;   // float [64] per-row factors
-constexpr int OFF_RED2 = OFF_FAC + ROWS * 4;               // float [GROUPS][4]
-constexpr int OFF_BAR = OFF_RED2 + GROUPS * 16;
+constexpr int OFF_BAR = OFF_FAC + ROWS * 4;
 constexpr int B_FULL = 0, B_EMPTY = B_FULL + RING, B_S = B_EMPTY + RING, B_P = B_S + 2,
               B_PV = B_P + 1, B_ROPE = B_PV + 1, B_Q = B_ROPE + 1, B_FIN = B_Q + 1, NUM_BARS = B_FIN + 1;
 constexpr int OFF_TMEM = OFF_BAR + NUM_BARS * 8;
@@ -204,12 +210,10 @@ __device__ __forceinline__ uint32_t e4m3x2_f16(uint32_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
   return h;
 }
-// largest x of a warp, through the order-preserving integer image of a float
-__device__ __forceinline__ float warp_max(float x) {
-  int i = __float_as_int(x);
-  i ^= (i >> 31) & 0x7fffffff;
-  i = __reduce_max_sync(0xffffffffu, i);
-  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ------------------------------------------------------------------ queries
@@ -245,8 +249,8 @@ struct QueryRow {
     }
     return __reduce_max_sync(0xffffffffu, m);
   }
-  // Writes the row's terms; returns its logit factor scale log2(e) 2^-k. bad: some element is not finite.
-  template <bool bad> __device__ __forceinline__ float stage(float scale, uint32_t top, int r, uint8_t* sp, int lane) const {
+  // Writes the row's terms; returns its logit factor 2^-k. bad: some element is not finite.
+  template <bool bad> __device__ __forceinline__ float stage(uint32_t top, int r, uint8_t* sp, int lane) const {
     const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
     *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
     // the power of two that brings the largest element into [128, 256)
@@ -279,7 +283,7 @@ struct QueryRow {
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     const float ra = __uint_as_float(rope << 16) * up, rb = __uint_as_float(rope & 0xffff0000u) * up;
     *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = pack_bf16x2(ra, rb);
-    return fminf(fmaxf(scale * LOG2E * __int_as_float((127 - e) << 23), 1.17549435e-38f), 3.402823466e38f);
+    return __int_as_float((127 - e) << 23);
   }
 };
 
@@ -512,7 +516,6 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     uint64_t* rmask = reinterpret_cast<uint64_t*>(sp + OFF_MASK) + g * GROUP_ROWS;
     float* fac = reinterpret_cast<float*>(sp + OFF_FAC) + g * GROUP_ROWS;
     float* red = reinterpret_cast<float*>(sp + OFF_RED) + g * 4 * GROUP_ROWS;
-    float* red2 = reinterpret_cast<float*>(sp + OFF_RED2) + g * 4;
     const uint32_t wg_bar = 1 + g;
     {
       // a warp stages four rows of its group, all loads in flight
@@ -525,10 +528,10 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       for (int k = 0; k < 4; ++k) bad |= top[k] >= 0x7f80u;          // (warp-uniform)
       if (bad) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<true>(a.scale, row[k].finite_magnitude(), 4 * warp + k, sp, lane);
+        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<true>(row[k].finite_magnitude(), 4 * warp + k, sp, lane);
       } else {                                       // four independent streams of instructions
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<false>(a.scale, top[k], 4 * warp + k, sp, lane);
+        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<false>(top[k], 4 * warp + k, sp, lane);
       }
       if (lane < 4) {
         const int r = 4 * warp + lane;
@@ -546,7 +549,6 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     float l[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) l[i] = 0.f;
-    float unit = 0.f, inv_unit = 0.f;                // the power of two that s_j is taken relative to
     const uint32_t quarter = tmem + ((uint32_t)(w * 32) << 16);
     const int key = w * 32 + lane;                   // also the dim of a block; the last quarter has no keys
     auto key_of = [&](int tile) { return key < KEYS ? k_lo + tile * KEYS + key : k_hi; };   // k_hi: no key
@@ -570,15 +572,17 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 
     for (int i = 0; i < NT; ++i) {
       if (g == 0 && slot == -2) record_error(a.d_err, KDV_DERR_BAD_SLOT);
-      const float s = finite(ks) ? ks : __int_as_float(0x7fc00000);   // a row of infinities has NaN logits
+      const float sr = ks * SCALE_UP;
+      const float s = finite(sr) ? ks : __int_as_float(0x7fc00000);   // a row of infinities has NaN logits
       const bool readable = slot >= 0;
       const int u = k_lo + i * KEYS + key - L;       // tree key if >= 0
       const bool plain = __all_sync(0xffffffffu, readable && u < 0);
       wait(bar(B_S + (i & 1)), (i >> 1) & 1);
       tc_fence_after();
+      const float sl = s * (a.scale * LOG2E);
       float t[16], d[16];
       bool dirty;
-      {                                              // t = s_j (q . k), -inf where the row does not see the key
+      {                                              // t = scale log2(e) s_j (q . k) 2^k, -inf where the row does not see the key
         uint32_t hi[16], lo[16];
         const uint32_t sb = quarter + TM_S + (i & 1) * 128 + GROUP_ROWS * g;
         tmem_ld16(sb, hi);
@@ -589,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         for (int r = 0; r < 16; r += 2) {
           float2 x = fma_f32x2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])), make_float2(0.0625f, 0.0625f),
                                make_float2(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1])));
-          x = mul_f32x2(x, make_float2(s, s));
+          x = mul_f32x2(x, make_float2(sl, sl));
           t[r] = x.x;
           t[r + 1] = x.y;
         }
@@ -601,7 +605,10 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
           }
         }
       }
-      auto exponents = [&]() {                       // d = log2 of the numerators; the largest
+      const float ls = fmaxf(lg2(fabsf(s)) + SCALE_UP_LOG2, SCALE_MIN);
+      // d = log2 of p; the largest. The rows' factors are powers of two, so a product is exact and the reference one
+      // of these products: the largest key's difference stays small at any size of the logits.
+      auto exponents = [&]() {
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
@@ -624,38 +631,30 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         }
       }
       // the first tile sets the reference in any case
-      const bool move = i == 0 || exponents() > P_GROW || fabsf(s) > unit;
+      const bool move = i == 0 || exponents() + ls > P_GROW;
       if (i == 0 || named_bar_or(wg_bar, 128, move)) {
         // ---- some reference moves: maxima over the tile's keys, per row
 #pragma unroll
         for (int r = 0; r < 16; r += 2) {
           const float4 f = cm[r / 2];
-          d[r] = t[r] * f.x;
-          d[r + 1] = t[r + 1] * f.y;
+          const float2 x = fma_f32x2(make_float2(t[r], t[r + 1]), make_float2(f.x, f.y), make_float2(ls, ls));
+          d[r] = x.x;
+          d[r + 1] = x.y;
         }
         const float mine = transpose_reduce(d, lane, [](float x, float y) { return fmaxf(x, y); });   // of row `lane`
         if (lane < GROUP_ROWS) red[w * GROUP_ROWS + lane] = mine;
-        const float smax = warp_max(isnan(s) ? 0.f : fabsf(s));
-        if (lane == 0) red2[w] = smax;
         named_bar_sync(wg_bar, 128);
         if (w == 0) {                                // one warp moves the rows' references
           const int row = lane & (GROUP_ROWS - 1);
           const float top = fmaxf(fmaxf(red[row], red[16 + row]), fmaxf(red[32 + row], red[48 + row]));   // NaN: no key moves it
           float* cr = reinterpret_cast<float*>(cm + row / 2) + (row & 1);
-          const float m_old = -cr[2], m_new = top - P_TOP > m_old ? top - P_TOP : m_old;
+          const float m_old = -cr[2], m_new = top - m_old > P_GROW ? top - P_TOP : m_old;   // a row's own keys decide
           __syncwarp();
           if (lane < GROUP_ROWS) {
             cr[2] = -m_new;
             fac[lane] = ex2(m_old - m_new);
           }
         }
-        // the scales' unit: the power of two at or above the largest, with room (2^-120 at least)
-        const float st = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
-        const uint32_t pow2 = max((__float_as_uint(st) + 0x7fffffu) & 0xff800000u, (127u - 120u) << 23);
-        const float unit_new = st > unit || unit == 0.f ? UNIT_ROOM * __uint_as_float(pow2) : unit;
-        inv_unit = 1.f / unit_new;
-        const float us = unit * inv_unit;
-        unit = unit_new;
         named_bar_sync(wg_bar, 128);
         if (i > 0) {
           wait(bar(B_PV), (i - 1) & 1);              // P.V of the tiles before is complete
@@ -668,14 +667,16 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
             tmem_ld16(quarter + x * ROWS + GROUP_ROWS * g, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * (fac[r] * us));
+            for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * fac[r]);
             tmem_st16(quarter + x * ROWS + GROUP_ROWS * g, o);
           }
           tmem_wait_st();
         }
         exponents();
+        // A reference of 2^24 and more is rounded to whole units.
+#pragma unroll
+        for (int r = 0; r < 16; ++r) d[r] = d[r] > P_GROW - ls ? P_GROW - ls : d[r];
       }
-      const float sr = s * inv_unit;
       uint32_t w0[4], w1[4], w2[4];                  // 16 rows = 16 bytes of each term
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4) {
@@ -729,9 +730,12 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       const float sum = (red[lane] + red[16 + lane]) + (red[32 + lane] + red[48 + lane]);
       const float m = -(reinterpret_cast<const float*>(cm + lane / 2) + (lane & 1))[2];
       const bool none = sum == 0.f;
-      const float inv = none ? 0.f : 1.f / sum;
+      const float inv = none ? 0.f : 1.f / sum / SCALE_UP;
       const float lse = none ? -INFINITY : LN2 * (m + log2f(sum));
-      fac[lane] = direct ? inv * unit : inv;
+      // a part's unit: a power of two
+      const float u = fminf(inv * (PART_UNIT * (float)(NT * KEYS)), 0x1p126f);
+      const float unit = none ? 1.f : __uint_as_float((__float_as_uint(u) + 0x7fffffu) & 0xff800000u);
+      fac[lane] = direct ? inv : inv * (1.f / unit);
       if (lane < nr) {
         if (!direct) a.part_s[orow0 + lane] = make_float2(lse, unit);
         else if (a.lse != nullptr) a.lse[orow0 + lane] = lse;

@@ -396,3 +396,73 @@ def test_millions_of_keys_through_shared_slots():
     e = np.abs(r.o.double().cpu().numpy() - o)
     assert np.all(e <= ob + 2.0 ** -9 * (np.abs(o) + ob) + 2.0 ** -24 * np.abs(o))
     assert np.all(np.abs(r.lse.double().cpu().numpy() - (lse + np.log(many))) <= lb + 2.0 ** -9)
+
+
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+@pytest.mark.parametrize("H", [64, 5])
+@pytest.mark.parametrize("scale", [1e30, 1e8, 2.0 ** -110])
+def test_unseen_scales_of_any_size_never_reach_an_output(impl, H, scale):
+    """Scales far from the others' in slots that a row does not see leave it as it was: with 64 heads, where
+    its 16 rows share no reference with the node that sees it, to the last bit; else within the bounds."""
+    c = plain8.Attn(34, [130, 0], [[-1, 0, 0, 1, 1, 2], [-1, 0, 0]], H)
+    clean = Run(c, impl).go().check()
+    node = int(c.table[c.kv_off[0] + 130 + 3])                        # seen by node 3 of request 0 alone
+    c.scale[np.append(np.setdiff1d(np.arange(c.slots), c.table), node)] = scale
+    r = Run(c, impl).go()
+    own = np.arange(3 * H, 4 * H)
+    rest = np.setdiff1d(np.arange(9 * H), own)
+    if H == 64:
+        assert torch.equal(r.o[rest], clean.o[rest]) and torch.equal(r.lse[rest], clean.lse[rest])
+    r.check(rows=rest)
+
+
+@pytest.mark.parametrize("splits", [1, 4])
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+def test_seen_key_of_a_large_scale_and_no_weight(impl, splits):
+    """One key of scale 2^14 (the others' are about 2^-6) whose logit is far below the rest takes no precision from them."""
+    c = plain8.Attn(35, [300], [[-1]], 64, paged=False)
+    c.scale[:] = 2.0 ** -6
+    # queries and the large key point away from one another; the other keys are as they were
+    c.q = (0.01 * c.q.float() + 1.0).bfloat16()
+    c.c8[150] = plain8.codes(np.full((1, c.D_c), -1.0), np.ones(1))
+    c.scale[150] = 2.0 ** 14
+    Run(c, impl, splits=splits).go().check()
+
+
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+def test_scales_that_differ_between_tiles(impl):
+    """Scales rise by 2^20 and fall by 2^40 from one part of the keys to the next, the logits staying moderate:
+    o is the large ones'; a request that holds small ones alone keeps its precision."""
+    c = plain8.Attn(36, [400, 200], [tree(2), tree(3)], 64, paged=False)
+    c.q = (2.0 ** -30 * c.q.float()).bfloat16()
+    e = np.full(c.slots, -6.0)
+    e[130:260] += 20
+    e[260:] -= 20
+    e[int(c.kv_off[1]):] = -60
+    c.scale[:] = np.exp2(e)
+    Run(c, impl).go().check()
+    Run(c, impl, splits=5).go().check()
+
+
+@pytest.mark.parametrize("impl", [AUTO, SIMT])
+@pytest.mark.parametrize("power", [27, 40, 90])
+def test_logits_beyond_the_exponents_precision(impl, power):
+    """Logits so large that neighbouring fp32 numbers are far apart: each row gives its largest key's values."""
+    c = plain8.Attn(37, [250], [tree(2)], 64, paged=False)
+    c.scale[:] = 2.0 ** -6
+    c.q = (2.0 ** power * c.q.float()).bfloat16()
+    o, lse, _, _ = c.answer()
+    r = Run(c, impl).go()
+    # A logit's products round by 80 2^-24 of their magnitudes, whose sums are below 8 times the row's largest logit here:
+    # a gap of 2^-9 of it leaves one key, off by the numerators' and the parts' steps.
+    vals = np.concatenate([plain8.code_values(c.c8), c.kr.to(torch.float64).numpy()], 1) * 2.0 ** -6
+    x = c.sm_scale * (c.q.to(torch.float64).numpy() @ vals.T)
+    for node in range(c.T[0]):
+        x[node * 64:(node + 1) * 64, [k for k in range(c.n[0]) if k not in set(c.node_keys(0, node))]] = -np.inf
+    y = np.sort(x, 1)
+    sure = y[:, -1] - y[:, -2] > 2.0 ** -9 * np.abs(y[:, -1])
+    assert sure.mean() > 0.5
+    got = r.o.double().cpu().numpy()
+    assert r.err.item() == 0 and np.isfinite(got).all() and torch.isfinite(r.lse).all()
+    assert np.all(np.abs(got - o)[sure] <= (2.0 ** -9 + 2.0 ** -11) * np.abs(o)[sure] + 2.0 ** -20)
+    assert np.all(np.abs(r.lse.double().cpu().numpy() - lse)[sure] <= 2.0 ** -9 * np.abs(lse)[sure])
