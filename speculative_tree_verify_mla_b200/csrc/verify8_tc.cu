@@ -47,10 +47,10 @@
 //
 // What bounds it: the tensor core and shared memory. A tile's 16 (N = 128) + 4 + 36 (N = 64) MMAs take
 // 2.55k clocks alone and 3.3k beside the copies and the softmax; one cp.async block of 12 KB takes
-// ~400. Over 200k keys the part runs into its power cap: 466 us in bursts, 545 us sustained (16
-// nodes x 64 heads, 956 and 818 TFLOP/s of the logical products). Contiguous pools through TMA
-// boxes instead of the gather: 486 and 556 us, so there is one way to bring keys in. Few rows over short contexts: 16k clocks an item
-// for set-up, queries, first tile and output, and the merge (4-7 us).
+// ~400. Over 200k keys the part runs into its power cap: 470 us in bursts, 550 us sustained (16
+// nodes x 64 heads, 948 and 810 TFLOP/s of the logical products). Contiguous pools through TMA
+// boxes instead of the gather: 20 and 11 us more, so there is one way to bring keys in. Few rows over short contexts: 16k
+// clocks an item for set-up, queries, first tile and output, and the merge (2.5-4 us): 13 nodes x 64 heads x 5.5k keys 26.5 us.
 #include <cuda_fp8.h>
 
 #include "sm100_ptx.cuh"
