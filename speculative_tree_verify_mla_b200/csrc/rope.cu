@@ -9,8 +9,9 @@
 // 64-bit angles are what a per-element version would spend its time on: a
 // head count of 64 would repeat each one 64 times), while the first vectors
 // are on their way, then streams the vectors through registers, four 16-byte units in flight a
-// thread. 8192 tokens x 64 heads x 128 dims, half of them rotated: 49 us (86 us with
-// the loads behind the table and a division for each unit).
+// thread. 8192 tokens x 64 heads x 128 dims, half of them rotated: 48.5 us (86 us with
+// the loads behind the table and a division for each unit). CTAs are small, so that some load while others store: 4096
+// tokens x 64 heads x 64 dims 11.0 us, 13.0 with 256 threads.
 #include <algorithm>
 #include <cmath>
 
@@ -19,8 +20,8 @@
 namespace kdv {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int TABLE = 2048;      // (cos, sin) entries a CTA holds (16 KB)
+constexpr int THREADS = 128;
+constexpr int TABLE = 1024;      // (cos, sin) entries a CTA holds (8 KB)
 constexpr int INFLIGHT = 4;      // units a thread loads before it stores the first
 
 struct RopeArgs {
@@ -334,9 +335,9 @@ kdv_status kdv_rope(const kdv_rope_params* p, void* stream) {
   const int V = vec ? 8 : 1, pairs = p->rot_dim / 2, apart = pairs / 8;
   const bool lanes = vec && half && (apart & (apart - 1)) == 0 && apart <= 16 && p->dim / 8 % (2 * apart) == 0;
   const int64_t units = (((half && !lanes) || V == 1) ? pairs / V : p->rot_dim / V) + (p->dim - p->rot_dim) / V;
-  // A CTA's units: one a thread until every SM has two CTAs, then up to as many as are in flight. 13 tokens x 64 heads
+  // A CTA's units: one a thread until every SM has four CTAs, then up to as many as are in flight. 13 tokens x 64 heads
   // x 64 dims: 2.4 us (3.2 in CTAs of four units a thread, of which there are 7); 416 tokens: 3.2 us (3.8).
-  const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(INFLIGHT, (int64_t)p->tokens * p->heads * units / (2 * 148 * THREADS)));
+  const int64_t deep = std::max<int64_t>(1, std::min<int64_t>(INFLIGHT, (int64_t)p->tokens * p->heads * units / (4 * 148 * THREADS)));
   const int64_t share = THREADS * deep;
   a.heads_per_cta = (int)std::max<int64_t>(1, std::min<int64_t>(p->heads, share / std::max<int64_t>(1, units)));
   a.group = a.heads_per_cta < p->heads
