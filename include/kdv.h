@@ -571,7 +571,11 @@ KDV_API kdv_status kdv_latent8_write(const kdv_latent8_params* p, void* stream);
  * The tensor-core kernel (KDV_IMPL_TC, AUTO's choice where it applies) takes
  * bf16 q, D_c = 512, D_r = 64, scale > 0, 16-byte aligned q, c8, kr, o and q rows;
  * KDV_IMPL_SIMT takes any D_c <= 512, D_r <= 64 and fp32 q. TC resolves weights times scales down to 2^-24 of a
- * row's largest; scales of 2^111 and more count as infinite there (NaN), those below 2^-108 lose precision.
+ * row's largest. Scales of 2^111 and more count as infinite there (NaN). Beside a key of scale s that holds a row's
+ * largest weight times scale, weights below 2^-118 s of its own count as none (felt from s = 2^94 on). Scales below
+ * 2^-108 lose precision (below 2^-100 in a split of more than 2^14 keys). Query rows of any magnitude keep theirs:
+ * latents to 2^-21 of the row's largest one, or to 2^-74 of its largest rope element where that is more; rows whose
+ * largest latent times scale is 2^123 or more count as infinite (NaN).
  */
 typedef struct kdv_verify8_params {
   int32_t batch;           /* B in [1, KDV_MAX_BATCH]                            */

@@ -28,6 +28,10 @@ struct Verify8Args {
   const uint64_t* mask;      // null: chain
   int32_t D_c, D_r;
   float scale;
+  // scale log2(e) = scale_part 2^scale_exponent for the tensor-core kernel, 2^-11 <= scale_part < 2^-9: a staged query row
+  // times a key is below 2^26, so with the key's scale, below 2^111, nothing overflows before the row's own power of two
+  float scale_part;
+  int32_t scale_exponent;
   int32_t q_f32, out_f32;
   void* o;
   float* lse;

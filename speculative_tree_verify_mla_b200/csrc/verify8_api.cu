@@ -215,6 +215,8 @@ kdv_status kdv_verify_attn8(const kdv_verify8_params* p, void* stream) {
   a.D_c = p->d_latent;
   a.D_r = p->d_rope;
   a.scale = p->scale;
+  a.scale_part = std::ldexp(std::frexp(p->scale, &a.scale_exponent) * 2.f * 1.4426950408889634f, -11);   // (0 stays 0)
+  a.scale_exponent += 10;
   a.q_f32 = p->dtype == KDV_F32;
   a.out_f32 = p->out_dtype == KDV_F32;
   a.o = p->o;

@@ -7,7 +7,8 @@
 // of memory and of shared memory, and nothing is converted:
 //   Q.K^T  q_lat times a power of two per row is split in two e4m3 terms,
 //          q = hi + lo / 16. bf16 holds 8 significant bits and a term 4, so the
-//          split is exact down to 2^-21 of the row's largest element. The rope
+//          split is exact down to 2^-21 of the row's largest latent element, whatever that is
+//          (beside a rope element 2^53 times as large: to 2^-74 of the rope element). The rope
 //          part is a bf16 product into the same sums. Products of e4m3 codes and
 //          their fp32 sums are exact to fp32's rounding (measured: 3e-8).
 //   P.V    p s_j is rounded to fp16 and split in three e5m2 terms, the first
@@ -75,6 +76,7 @@ constexpr int THREADS = (FIRST_PRODUCER + PRODUCER_WARPS) * 32;   // 640: 96 reg
 // 27.0 with a reference set to 10, 28.9 with 12: references move less often)
 constexpr float P_TOP = 8.f, P_GROW = 15.f;
 // Scales are taken times 2^16: those of 2^-108 to 2^111 have room, smaller ones lose precision and larger ones count as infinite.
+// (p = 2^8 / (2^16 s) for the key that sets the reference, and ex2 flushes below 2^-126: from s = 2^94 on the smallest weights go.)
 constexpr float SCALE_UP = 65536.f, SCALE_UP_LOG2 = 16.f;
 constexpr float SCALE_MIN = -92.f;           // log2 of the least that a reference counts: p stays below 2^107, sums of 2^20 in fp32
 // |o| <= 448 n 2^15 / l for n keys: 57344 in units of 256 n / l. Where one key of a part holds all the weight, p s >= 2^8
@@ -82,7 +84,7 @@ constexpr float SCALE_MIN = -92.f;           // log2 of the least that a referen
 // (A second bound, by the largest scale seen, would lift that for 0.5 us of a 5.5k layer's 26.5.)
 constexpr float PART_UNIT = 256.f;
 constexpr float NO_MAX = -1e30f;             // the reference of a row that has seen no key
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LN2 = 0.6931471805599453f;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
 constexpr uint32_t POLLS = 64;               // between two looks at the clock,
 constexpr uint64_t SHORT_NS = 100000;        // unless the limit is shorter than they may take
@@ -219,7 +221,13 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// 2^k: infinite where it is no float, 2^-149 at least (the product with a logit of -inf has to stay that)
+__device__ __forceinline__ float power_of_two(int k) {
+  return __int_as_float(k > 127 ? 0x7f800000 : k >= -126 ? (k + 127) << 23 : 1 << max(k + 149, 0));
+}
+
 // ------------------------------------------------------------------ queries
+constexpr uint32_t PLAIN_LATENT = (127 - 21) << 7, PLAIN_ROPE = (127 + 32) << 7;   // bf16 bits of 2^-21 and 2^32
 // One row by one warp: lane l holds latent elements 16 l .. 16 l + 15 and rope
 // elements 2 l, 2 l + 1.
 struct QueryRow {
@@ -252,13 +260,26 @@ struct QueryRow {
     }
     return __reduce_max_sync(0xffffffffu, m);
   }
-  // Writes the row's terms; returns its logit factor 2^-k. bad: some element is not finite.
-  template <bool bad> __device__ __forceinline__ float stage(uint32_t top, int r, uint8_t* sp, int lane) const {
+  // The magnitudes of this lane's rope elements.
+  __device__ __forceinline__ uint32_t rope_magnitudes() const { return rope & 0x7fff7fffu; }
+  // The exponent of the power of two that the row is staged times. Plain rows: largest latent element of 2^-21 or more,
+  // which comes into [128, 256) (or a row of zeros), rope elements below 2^32.
+  __device__ __forceinline__ static bool plain(uint32_t top) { return top == 0u || (top >= PLAIN_LATENT && top < 0x7f80u); }
+  __device__ __forceinline__ static int plain_exponent(uint32_t top) { return top == 0u ? 0 : 7 + 127 - (int)(top >> 7); }
+  // Any row: the same of its finite elements, but rope elements stay below 2^61. A row without latents goes by its rope part.
+  __device__ __forceinline__ int any_exponent() const {
+    const uint32_t lat = finite_magnitude(), lo = rope & 0x7fffu, hi = (rope >> 16) & 0x7fffu;
+    const uint32_t rp = __reduce_max_sync(0xffffffffu, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+    auto exponent = [](uint32_t m) { return m >= 0x80u ? (int)(m >> 7) - 127 : -102 - __clz(m); };   // floor(log2), m > 0
+    if (lat == 0u) return rp == 0u ? 0 : 7 - exponent(rp);
+    return rp == 0u ? 7 - exponent(lat) : min(7 - exponent(lat), 60 - exponent(rp));
+  }
+  // Writes the row's terms times 2^e. bad: some element is not finite, or 2^e is no float.
+  template <bool bad> __device__ __forceinline__ void stage(int e, int r, uint8_t* sp, int lane) const {
     const uint32_t blk = (uint32_t)(lane / 8) * QBLOCK, col = (uint32_t)(lane % 8) * 16;
     *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128((r + ROWS) * 128 + lane * 4)) = 0u;
-    // the power of two that brings the largest element into [128, 256)
-    const int e = top == 0u ? 0 : max(-120, min(60, 7 + 127 - (int)(top >> 7)));
-    const float up = __int_as_float((e + 127) << 23);
+    const int first = bad ? min(e, 100) : e;              // -120 <= e <= 140: in two steps
+    const float up = __int_as_float((first + 127) << 23), rest = bad ? __int_as_float((e - first + 127) << 23) : 1.f;
     // (fp16 holds the scaled elements: exact down to 2^-14, off by 2^-25 at most below)
     uint32_t hi[4], lo[4];
     const __half2 sixteen = __float2half2_rn(16.f);
@@ -268,6 +289,8 @@ struct QueryRow {
       for (int j = 0; j < 2; ++j) {
         float x0 = __uint_as_float(u[2 * i + j] << 16) * up, x1 = __uint_as_float(u[2 * i + j] & 0xffff0000u) * up;
         if (bad) {
+          x0 *= rest;
+          x1 *= rest;
           x0 = finite(x0) ? x0 : __int_as_float(0x7fc00000);
           x1 = finite(x1) ? x1 : __int_as_float(0x7fc00000);
         }
@@ -284,9 +307,8 @@ struct QueryRow {
     }
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128(r * 128 + col)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(sp + OFF_Q + blk + swz128((r + ROWS) * 128 + col)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    const float ra = __uint_as_float(rope << 16) * up, rb = __uint_as_float(rope & 0xffff0000u) * up;
+    const float ra = __uint_as_float(rope << 16) * up * rest, rb = __uint_as_float(rope & 0xffff0000u) * up * rest;
     *reinterpret_cast<uint32_t*>(sp + OFF_QR + swz128(r * 128 + lane * 4)) = pack_bf16x2(ra, rb);
-    return __int_as_float((127 - e) << 23);
   }
 };
 
@@ -522,24 +544,34 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
     const uint32_t wg_bar = 1 + g;
     {
       // a warp stages four rows of its group, all loads in flight
-      float c[4] = {1.f, 1.f, 1.f, 1.f};
-      uint32_t top[4];
-      bool bad = false;
+      int e[4];
+      uint32_t top[4], rope = 0;
+      bool odd = false;
 #pragma unroll
       for (int k = 0; k < 4; ++k) top[k] = row[k].magnitude();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) bad |= top[k] >= 0x7f80u;          // (warp-uniform)
-      if (bad) {
+      for (int k = 0; k < 4; ++k) {
+        rope = __vmaxu2(rope, row[k].rope_magnitudes());
+        odd |= !QueryRow::plain(top[k]) || (top[k] == 0u && row[k].rope_magnitudes() != 0u);
+      }
+      odd |= (rope & 0xffffu) >= PLAIN_ROPE || (rope >> 16) >= PLAIN_ROPE;
+      if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<true>(row[k].finite_magnitude(), 4 * warp + k, sp, lane);
+        for (int k = 0; k < 4; ++k) {
+          e[k] = row[k].any_exponent();
+          row[k].stage<true>(e[k], 4 * warp + k, sp, lane);
+        }
       } else {                                       // four independent streams of instructions
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = row[k].stage<false>(top[k], 4 * warp + k, sp, lane);
+        for (int k = 0; k < 4; ++k) {
+          e[k] = QueryRow::plain_exponent(top[k]);
+          row[k].stage<false>(e[k], 4 * warp + k, sp, lane);
+        }
       }
       if (lane < 4) {
         const int r = 4 * warp + lane;
         float* f = reinterpret_cast<float*>(sp + OFF_CM) + (r / 2) * 4 + (r & 1);
-        f[0] = lane == 0 ? c[0] : lane == 1 ? c[1] : lane == 2 ? c[2] : c[3];
+        f[0] = power_of_two(a.scale_exponent - (lane == 0 ? e[0] : lane == 1 ? e[1] : lane == 2 ? e[2] : e[3]));
         f[2] = -NO_MAX;
         reinterpret_cast<uint64_t*>(sp + OFF_MASK)[r] = qmask;
       }
@@ -582,10 +614,10 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       const bool plain = __all_sync(0xffffffffu, readable && u < 0);
       wait(bar(B_S + (i & 1)), (i >> 1) & 1);
       tc_fence_after();
-      const float sl = s * (a.scale * LOG2E);
+      const float sl = s * a.scale_part;
       float t[16], d[16];
       bool dirty;
-      {                                              // t = scale log2(e) s_j (q . k) 2^k, -inf where the row does not see the key
+      {                                              // t = scale_part s_j (q . k) 2^e, -inf where the row does not see the key
         uint32_t hi[16], lo[16];
         const uint32_t sb = quarter + TM_S + (i & 1) * 128 + GROUP_ROWS * g;
         tmem_ld16(sb, hi);
@@ -609,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
         }
       }
       const float ls = fmaxf(lg2(fabsf(s)) + SCALE_UP_LOG2, SCALE_MIN);
-      // d = log2 of p; the largest. The rows' factors are powers of two, so a product is exact and the reference one
+      // d = log2 of p; the largest. The rows' factors 2^(scale_exponent - e) are powers of two, so a product is exact and the reference one
       // of these products: the largest key's difference stays small at any size of the logits.
       auto exponents = [&]() {
         float top = -INFINITY;

@@ -1,0 +1,126 @@
+"""Attention over the 8-bit cache on the tensor cores at the ends of its ranges,
+against the 64-bit form with bounds of its own, counted before the first run.
+
+A logit: the split of q is exact for elements down to 2^-13 of the row's largest
+latent one and off by 2^-21 of that largest one below. 16 matrix instructions add 32
+products of codes each and 4 add 16 of the rope part; each may round its sum by
+2^-23 of the magnitudes that it adds up, 40 2^-24 in all, and joining the two
+terms, the key's factor (two roundings) and the product with it are 4 2^-24 more.
+The exponent's argument rounds at 2^-24 of its terms, twice.
+
+A numerator is rounded to 2^-9 of itself, and to half of e5m2's least step, 2^-17,
+where a row's largest is at least 2^8 by then: 2^-25 of the largest one so far. A
+stored part is fp16 (2^-11) in a unit that leaves at most keys 2^-24 of its largest
+weight times scale as an absolute step."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_tree_verify_mla_b200 import kdv
+from tests import plain8
+from tests.test_gpu_verify8 import Run
+
+pytestmark = pytest.mark.gpu
+TILE = 96
+TC = kdv.KDV_IMPL_TC
+
+
+def form(q, codes, rope, s, sm, times=None, part_keys=0, running=True):
+    """(o, lse, bound of o, bound of lse, weights times multiplicity) of rows that see all n keys, in the kernel's
+    key order. times: how often each key occurs. part_keys: keys of a stored part, 0 where o is written directly.
+    running: a numerator's least step follows the largest one so far, else the largest one of all."""
+    times = np.ones(len(s)) if times is None else times
+    k = np.concatenate([codes, rope], 1) * s[:, None]
+    aq, ak = np.abs(q), np.abs(k)
+    x, size = sm * (q @ k.T), sm * (aq @ ak.T)
+    big = aq[:, :512].max(1, keepdims=True)
+    lost = sm * 2.0 ** -21 * big * ((aq[:, :512] < 2.0 ** -13 * big) @ ak[:, :512].T)
+    top = x.max(1, keepdims=True)
+    e = np.exp(x - top)
+    l = (e * times).sum(1, keepdims=True)
+    w = e * times / l
+    eps = 44 * 2.0 ** -24 * size + lost + 2.0 ** -22 * np.maximum(np.abs(x), np.abs(top)) + 2.0 ** -20
+    ws = e * np.abs(s) / l
+    if running:
+        tops = np.stack([ws[:, i:i + TILE].max(1) for i in range(0, len(s), TILE)], 1)
+        most = np.repeat(np.maximum.accumulate(tops, 1), TILE, 1)[:, :len(s)]
+    else:
+        most = ws.max(1, keepdims=True)
+    step = 2.0 ** -9 + (2.0 ** -11 if part_keys else 0.0) + 2 * eps
+    o = w @ k[:, :512]
+    ob = (w * step) @ ak[:, :512] + (2.0 ** -25 * most * times) @ np.abs(codes)
+    if part_keys:
+        ob = ob + 2.0 ** -24 * part_keys * ws.max(1, keepdims=True)
+    lse = (top + np.log(l))[:, 0]
+    return o, lse, ob + 2.0 ** -20 * np.abs(o), (w * eps).sum(1) + 2.0 ** -22 * np.abs(lse) + 2.0 ** -20, w
+
+
+def of(c, b=0):
+    """q, codes, rope parts and scales of request b's keys in their order, 64 bits."""
+    keys = np.arange(c.kv_off[b], c.kv_off[b + 1])
+    slot = c.table[keys] if c.table is not None else keys
+    s = np.repeat(c.scale.astype(np.float64), c.block)[slot]
+    r = slice(int(c.tree_off[b]) * c.H, int(c.tree_off[b + 1]) * c.H)
+    return c.q.to(torch.float64).numpy()[r], plain8.code_values(c.c8[slot]), c.kr.to(torch.float64).numpy()[slot], s
+
+
+def compare(run, o, lse, ob, lb):
+    assert run.err.item() == 0
+    got, gl = run.o.double().cpu().numpy(), run.lse.double().cpu().numpy()
+    e, el = np.abs(got - o), np.abs(gl - lse)
+    assert np.all(el <= lb), float((el / lb).max())
+    assert np.all(e <= ob), float((e / np.maximum(ob, 1e-300)).max())
+
+
+def one_token(seed, n, H=64):
+    """One token of H heads over n keys (itself the last one), keys where they lie."""
+    return plain8.Attn(seed, [n - 1], [[-1]], H, paged=False)
+
+
+@pytest.mark.parametrize("how,e", [("keys", e) for e in (100, 60, -40, -60, -72, -98)]
+                         + [("scale", e) for e in (100, 40, -60, -72, -100, -118, -130)])
+def test_queries_of_any_magnitude(how, e):
+    """Queries of 2^e, with the keys' scales or the softmax scale of 2^-e: the same logits, the same accuracy.
+    (At 2^-130 they are subnormal and hold two or three bits each, which then count.)"""
+    c = one_token(60, 300)
+    c.q = (c.q.double() * 2.0 ** e).bfloat16()
+    if how == "keys":
+        c.scale = (c.scale * 2.0 ** -e).astype(np.float32)
+    else:
+        c.sm_scale = float(np.float32(c.sm_scale * 2.0 ** -e))
+    for splits in (1, 2):
+        f = form(*of(c), c.sm_scale, part_keys=192 if splits == 2 else 0, running=splits == 1)
+        assert np.ptp(f[4], 1).min() > 2.0 ** -12                     # the logits differ
+        compare(Run(c, TC, splits=splits).go(), *f[:4])
+
+
+def test_queries_of_many_magnitudes_in_a_tile():
+    """Rows of 2^0 to 2^-132 beside one another: the small ones weigh all keys alike."""
+    c = one_token(61, 200)
+    c.q = (c.q.double() * torch.tensor([2.0 ** -(12 * (r % 12)) for r in range(64)], dtype=torch.float64)[:, None]).bfloat16()
+    compare(Run(c, TC, splits=1).go(), *form(*of(c), c.sm_scale)[:4])
+    c.sm_scale = 2.0 ** 60                                            # rows of 2^-60 have moderate logits, those above one key
+    q, codes, rope, s = of(c)
+    r = np.flatnonzero(np.array([12 * (r % 12) for r in range(64)]) >= 60)
+    o, lse, ob, lb, _ = form(q[r], codes, rope, s, c.sm_scale)
+    run = Run(c, TC, splits=1).go()
+    run.o, run.lse = run.o[r.tolist()], run.lse[r.tolist()]
+    compare(run, o, lse, ob, lb)
+
+
+@pytest.mark.parametrize("lat,rope,rope_keys", [(-45, 0, False), (-100, -60, False), (-100, -100, True), (None, -100, True), (None, 0, True),
+                                                (38, 40, True), (None, -126, True), (-60, 10, True), (-110, 5, True)])
+def test_latent_and_rope_parts_of_different_magnitudes(lat, rope, rope_keys):
+    """q_lat of 2^lat (None: zeros) beside q_rope of 2^rope, the softmax scale bringing the part that counts back: the latent
+    one where the keys' rope parts are zeros (rope_keys False), else the larger one."""
+    c = one_token(62, 250)
+    q = c.q.double()
+    q[:, :512] *= 0.0 if lat is None else 2.0 ** lat
+    q[:, 512:] *= 2.0 ** rope
+    c.q = q.bfloat16()
+    if not rope_keys:
+        c.kr = torch.zeros_like(c.kr)
+    c.sm_scale = float(np.float32(c.sm_scale * 2.0 ** -(rope if lat is None or rope_keys and rope > lat else lat)))
+    f = form(*of(c), c.sm_scale)
+    assert np.ptp(f[4], 1).min() > 2.0 ** -12
+    compare(Run(c, TC, splits=1).go(), *f[:4])
