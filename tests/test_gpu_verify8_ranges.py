@@ -124,3 +124,64 @@ def test_latent_and_rope_parts_of_different_magnitudes(lat, rope, rope_keys):
     f = form(*of(c), c.sm_scale)
     assert np.ptp(f[4], 1).min() > 2.0 ** -12
     compare(Run(c, TC, splits=1).go(), *f[:4])
+
+
+def moves(ws):
+    """How often a row's reference moves behind its first tile: ws log2 of the weights times scales, rows x keys."""
+    n = np.zeros(len(ws), dtype=int)
+    m = ws[:, :TILE].max(1) - 8.0
+    for i in range(TILE, ws.shape[1], TILE):
+        top = ws[:, i:i + TILE].max(1)
+        go = top - m > 15.0
+        m, n = np.where(go, top - 8.0, m), n + go
+    return n
+
+
+def steps(seed, level, flat=False):
+    """One token over tiles whose largest weight times scale is about 2^(8 level): by their logits, or (flat) by their scales
+    alone. Tile i's keys have 44 dims to themselves, so a tile's share of the output is seen whatever the others weigh."""
+    n = len(level) * TILE
+    c = one_token(seed, n)
+    rng = np.random.default_rng(seed)
+    t = np.repeat(np.arange(len(level)), TILE)
+    lv = np.repeat(np.array(level), TILE)
+    v = np.zeros((n, 512))
+    for i in range(len(level)):
+        v[t == i, 44 * i:44 * i + 44] = 100 + 20 * rng.standard_normal((TILE, 44))
+    q = np.zeros((64, 576))
+    if flat:
+        c.scale = np.exp2(-40.0 + 8 * lv).astype(np.float32)
+        q[:, 512:] = rng.standard_normal((64, 64)) * 2.0 ** (36 - 8 * max(level))
+    else:
+        c.scale = np.full(n, 2.0 ** -6, np.float32)
+        v[:, 448:] = 32 * lv[:, None]
+        q[:, 448:512] = (1 + np.arange(64) / 2000)[:, None] * 5.5 / (c.sm_scale * 32)
+        q[:, 512:] = rng.standard_normal((64, 64)) * 0.3
+    c.c8 = plain8.codes(v, np.ones(n))
+    c.q = torch.from_numpy(q.astype(np.float32)).bfloat16()
+    return c
+
+
+def log2_ws(c):
+    q, codes, rope, s = of(c)
+    return c.sm_scale * (q @ (np.concatenate([codes, rope], 1) * s[:, None]).T) / np.log(2) + np.log2(s)
+
+
+@pytest.mark.parametrize("flat", [False, True])
+def test_references_that_move_in_every_tile(flat):
+    """Ten tiles, each 2^8 above the one before, by logits or by scales: each one's share of o and lse comes through
+    all the moves behind it."""
+    c = steps(63, list(range(10)), flat)
+    n = moves(log2_ws(c))
+    assert n.min() >= 8, n
+    compare(Run(c, TC, splits=1).go(), *form(*of(c), c.sm_scale)[:4])
+    compare(Run(c, TC, splits=3).go(), *form(*of(c), c.sm_scale, part_keys=384, running=False)[:4])
+
+
+@pytest.mark.parametrize("flat", [False, True])
+def test_references_that_rise_and_stay(flat):
+    """The same up to the middle and down again: five moves, none behind the middle."""
+    c = steps(64, [0, 1, 2, 3, 4, 5, 4, 3, 2, 1], flat)
+    n = moves(log2_ws(c))
+    assert np.all(n == 5), n
+    compare(Run(c, TC, splits=1).go(), *form(*of(c), c.sm_scale)[:4])
