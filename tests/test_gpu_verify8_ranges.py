@@ -18,7 +18,7 @@ import torch
 
 from speculative_tree_verify_mla_b200 import kdv
 from tests import plain8
-from tests.test_gpu_verify8 import Run
+from tests.test_gpu_verify8 import Run, i32
 
 pytestmark = pytest.mark.gpu
 TILE = 96
@@ -185,3 +185,40 @@ def test_references_that_rise_and_stay(flat):
     n = moves(log2_ws(c))
     assert np.all(n == 5), n
     compare(Run(c, TC, splits=1).go(), *form(*of(c), c.sm_scale)[:4])
+
+
+@pytest.mark.parametrize("many", [6, 128])
+@pytest.mark.parametrize("splits", [1, 0])
+def test_a_sink_that_holds_half_and_a_tail_that_holds_the_rest(many, splits):
+    """One key with half of the weight, then 1000 slots that the page table names `many` times over: 2^-12.5 and 2^-17 of the
+    sink each. The tail's codes have a mean in 64 dims, so an answer without it is far off."""
+    c = plain8.Attn(65, [1000], [[-1]], 16, paged=False)
+    rng = np.random.default_rng(65)
+    v = np.zeros((1001, 512))
+    v[1:, :64] = 100 + 60 * rng.standard_normal((1000, 64))
+    v[1:, 64:256] = 60 * rng.standard_normal((1000, 192))
+    v[0, :64], v[0, 64:256], v[0, 256:] = -200.0, 60 * rng.standard_normal(192), 256.0
+    c.c8 = plain8.codes(v, np.ones(1001))
+    c.scale = np.full(1001, 2.0 ** -6, np.float32)
+    q = np.zeros((16, 576))
+    q[:, :256] = 0.02 * rng.standard_normal((16, 256))
+    q[:, 512:] = 0.02 * rng.standard_normal((16, 64))
+    _, codes, rope, s = of(c)
+    k = np.concatenate([codes, rope], 1) * s[:, None]
+    # the sink's logit: ln of the tail's sum of weights, by the dims that it has to itself
+    x = c.sm_scale * (q @ k.T)
+    q[:, 256:512] = ((np.log(many * np.exp(x[:, 1:]).sum(1)) - x[:, 0]) / (c.sm_scale * 256 * 4.0))[:, None]
+    c.q = torch.from_numpy(q.astype(np.float32)).bfloat16()
+    times = np.concatenate([[1.0], np.full(1000, float(many))])
+    n = 1000 * many + 1                                               # keys: the sink, then the slots over and over
+    table = i32(np.concatenate([[0], np.tile(np.arange(1, 1001), many)]))
+    f = form(*of(c), c.sm_scale, times=times, part_keys=0 if splits == 1 else n, running=False)
+    assert np.all((f[4][:, 0] > 0.4) & (f[4][:, 0] < 0.6))
+    alone = np.abs(k[0, :512] - f[0])
+    assert np.all(alone[:, :64] > 8 * f[2][:, :64])                   # the sink's row alone does not pass
+    r = Run(c, TC, splits=splits, page_table=table, kv_off=i32([0, n]), prefix_len=i32([n - 1]), h_prefix_len=[n - 1])
+    size = kdv.kdv_verify_attn8_workspace(r.p)
+    r.ws = torch.zeros(max(16, size), dtype=torch.uint8, device="cuda")
+    r.p.workspace, r.p.workspace_bytes = r.ws.data_ptr(), size
+    # sums of n / 32 equal terms a lane round by 2^-24 of themselves each time, to one side at worst
+    compare(r.go(), f[0], f[1], f[2] + 2.0 ** -24 * (n / 32) * np.abs(f[0]), f[3] + 2.0 ** -24 * (n / 32))
