@@ -58,15 +58,16 @@ __device__ inline bool request_ok(const Verify8Args& a, const VerifyPlan& p, int
   return ok;
 }
 
-// Raises a kernel's dynamic shared memory limit, once for each device.
-inline cudaError_t allow_smem(const void* kernel, int bytes) {
+// Raises a kernel's dynamic shared memory limit to the most that its launches take, once for each kernel and device.
+// (The limit is the kernel's, whoever launches it: one that a call lowers is missing in another thread's launch.)
+template <auto Kernel> cudaError_t allow_smem(int bytes) {
   static std::atomic<uint64_t> done[4];                    // devices below 256
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const bool known = dev >= 0 && dev < 256;
   if (known && (done[dev / 64].load(std::memory_order_acquire) >> (dev % 64)) & 1u) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e == cudaSuccess && known) done[dev / 64].fetch_or(1ull << (dev % 64), std::memory_order_release);
   return e;
 }

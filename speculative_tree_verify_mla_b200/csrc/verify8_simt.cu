@@ -16,6 +16,7 @@ namespace {
 constexpr int KT = 32;                 // keys per shared-memory tile
 constexpr int WARPS = SIMT_ROWS;       // one warp per query row
 constexpr int DC_PER_LANE = 16;        // D_c <= 512
+constexpr int smem_bytes(int D_q) { return (KT * (D_q + 1) + WARPS * D_q) * (int)sizeof(float); }
 
 __device__ inline float code_value(uint8_t c) {
   __nv_fp8_e4m3 v;
@@ -342,12 +343,12 @@ __global__ void __launch_bounds__(ROW_WARPS * 32) combine8_rows_kernel(const __g
 }  // namespace
 
 cudaError_t launch_verify8_simt(const Verify8Args& a, const VerifyPlan& p, cudaStream_t stream) {
-  const int D_q = a.D_c + a.D_r;
-  const size_t smem = (size_t)(KT * (D_q + 1) + WARPS * D_q) * sizeof(float);
-  auto k = a.q_f32 ? verify8_simt_kernel<float> : verify8_simt_kernel<__nv_bfloat16>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr int MOST = smem_bytes(512 + 64);
+  const int smem = smem_bytes(a.D_c + a.D_r);
+  cudaError_t e = a.q_f32 ? allow_smem<verify8_simt_kernel<float>>(MOST) : allow_smem<verify8_simt_kernel<__nv_bfloat16>>(MOST);
   if (e != cudaSuccess) return e;
-  k<<<p.n_items, WARPS * 32, smem, stream>>>(a, p);
+  if (a.q_f32) verify8_simt_kernel<float><<<p.n_items, WARPS * 32, smem, stream>>>(a, p);
+  else verify8_simt_kernel<__nv_bfloat16><<<p.n_items, WARPS * 32, smem, stream>>>(a, p);
   return cudaGetLastError();
 }
 

@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
 }  // namespace
 
 cudaError_t launch_verify8_tc(const Verify8Args& a, const VerifyPlan& p, cudaStream_t stream) {
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(verify8_tc_kernel), SMEM_BYTES);
+  cudaError_t e = allow_smem<verify8_tc_kernel>(SMEM_BYTES);
   if (e != cudaSuccess) return e;
   // a programmatic dependent: it waits itself, before its first read
   cudaLaunchConfig_t cfg = {};
