@@ -644,7 +644,8 @@ typedef struct kdv_logits_params {
   const int32_t* hist;     /* [B][hist_ld] committed tokens, nullable            */
   int64_t hist_ld;
   const int32_t* hist_len;     /* [B] device, with hist                          */
-  const int32_t* prompt_len;   /* [B] device, nullable (0: all of it was made)   */
+  const int32_t* prompt_len;   /* [B] device, nullable (0: all of it was made); from hist_len on
+                                  all of the history is prompt                   */
   const float* repetition;     /* [B] device, nullable (1); finite and > 0       */
   const float* presence;       /* [B] device, nullable (0)                       */
   const float* frequency;      /* [B] device, nullable (0)                       */

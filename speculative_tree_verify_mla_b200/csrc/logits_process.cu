@@ -203,7 +203,7 @@ __device__ __forceinline__ void process_tile(const LogitsArgs& a, uint32_t* coun
   }
   // history: made tokens add 2, prompt tokens set bit 0
   if (a.hist != nullptr) {
-    if (len < 0 || len > a.hist_ld || pl < 0) {
+    if (len < 0 || len > a.hist_ld || pl < 0 || pl > a.hist_ld) {   // (pl needs no clamp: i < len <= hist_ld)
       if (reports && tid == 0) record_error(a.d_err, KDV_DERR_BAD_LENGTH);
       len = (int)min((int64_t)max(len, 0), a.hist_ld);
     }
