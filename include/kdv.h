@@ -484,8 +484,8 @@ typedef struct kdv_rope_params {
   int64_t x_token_stride;
   int64_t x_head_stride;   /* |stride| >= dim when heads > 1                     */
   void* y;                 /* out; may be x itself with its strides and type, no other overlap */
-  int64_t y_token_stride;
-  int64_t y_head_stride;
+  int64_t y_token_stride;  /* any strides that write no element twice            */
+  int64_t y_head_stride;   /* (others: KDV_ERR_INVALID_ARG)                      */
   const int32_t* pos;      /* [n] positions (any int32), or NULL: token i is tree node i and
                               pos = prefix_len[b] + depth[i] of its request b    */
   int32_t batch;           /* with pos NULL: B in [1, KDV_MAX_BATCH]             */

@@ -235,6 +235,21 @@ void launch_typed(const RopeArgs& a, const RopeTurns<KDV_MAX_ROT / 2>& f, bool h
   }
 }
 
+// Whether two of the n x m vectors of dim elements at i * s + j * t (i < n, j < m) overlap; s and t >= 0.
+bool vectors_overlap(int64_t n, int64_t s, int64_t m, int64_t t, int64_t dim) {
+  if (n > m) return vectors_overlap(m, t, n, s, dim);
+  if (m > 1 && t < dim) return true;
+  if (n == 1 || (__int128)s >= (__int128)(m - 1) * t + dim) return false;            // whole rows apart,
+  if (s >= dim && (__int128)t >= (__int128)(n - 1) * s + dim) return false;         // or whole columns
+  for (int64_t i = 1; i < n; ++i) {                     // i s apart along one axis: against the nearest multiples of t
+    const __int128 d = (__int128)i * s;
+    const __int128 j = m > 1 ? d / t : 0;
+    if (j >= m) return false;                           // behind the last vector, by t or more; so are all the others
+    if (d - j * t < dim || (j + 1 < m && (j + 1) * t - d < dim)) return true;
+  }
+  return false;
+}
+
 bool rows16(const void* p, int64_t ts, int64_t hs, int esz) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ts * esz) % 16 == 0 && (hs * esz) % 16 == 0;
 }
@@ -296,11 +311,14 @@ kdv_status kdv_rope(const kdv_rope_params* p, void* stream) {
   if (p->h_inv_freq == nullptr || !std::isfinite(p->mscale)) return KDV_ERR_INVALID_ARG;
   for (int k = 0; k < p->rot_dim / 2; ++k)
     if (!std::isfinite(p->h_inv_freq[k])) return KDV_ERR_INVALID_ARG;
+  for (const int64_t stride : {p->x_head_stride, p->y_token_stride, p->y_head_stride})
+    if (stride == INT64_MIN) return KDV_ERR_INVALID_ARG;                // (has no magnitude)
   if (p->heads > 1 && (std::llabs(p->x_head_stride) < p->dim || std::llabs(p->y_head_stride) < p->dim))
     return KDV_ERR_INVALID_ARG;
   if (p->tokens == 0) return KDV_OK;
   if (p->x == nullptr || p->y == nullptr) return KDV_ERR_INVALID_ARG;
-  if (p->tokens > 1 && std::llabs(p->y_token_stride) < p->dim) return KDV_ERR_INVALID_ARG;   // rows written twice
+  if (vectors_overlap(p->tokens, std::llabs(p->y_token_stride), p->heads, std::llabs(p->y_head_stride), p->dim))
+    return KDV_ERR_INVALID_ARG;                                         // elements written twice
   const int xe = p->x_dtype == KDV_BF16 ? 2 : 4, ye = p->y_dtype == KDV_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(p->x) % xe || reinterpret_cast<uintptr_t>(p->y) % ye) return KDV_ERR_INVALID_ARG;
   if (p->x == p->y && (xe != ye || (p->tokens > 1 && p->x_token_stride != p->y_token_stride) ||
