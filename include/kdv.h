@@ -487,7 +487,8 @@ typedef struct kdv_rope_params {
   int64_t y_token_stride;  /* any strides that write no element twice            */
   int64_t y_head_stride;   /* (others: KDV_ERR_INVALID_ARG)                      */
   const int32_t* pos;      /* [n] positions (any int32), or NULL: token i is tree node i and
-                              pos = prefix_len[b] + depth[i] of its request b    */
+                              pos = prefix_len[b] + depth[i] of its request b (0
+                              where no request holds it)                         */
   int32_t batch;           /* with pos NULL: B in [1, KDV_MAX_BATCH]             */
   const int32_t* tree_off; /* [B+1] device CSR over the n nodes                  */
   const int32_t* prefix_len;   /* [B] device                                     */
@@ -522,7 +523,8 @@ KDV_API kdv_status kdv_rope(const kdv_rope_params* p, void* stream);
  * even. A c value that is NaN or infinite is stored as the e4m3 NaN and reported
  * (KDV_DERR_RANGE; it is left out of amax). KDV_DERR_BAD_SLOT: slot outside
  * [0, num_slots), row not written. KDV_DERR_BAD_LENGTH: a node beyond its
- * request's kv_off range or outside tree_off. Two rows of one call given the
+ * request's kv_off range, or a row outside tree_off that takes its slot or its
+ * position from the tree, row not written. Two rows of one call given the
  * same slot leave that slot unspecified (some mix of the two), others are right.
  */
 typedef struct kdv_latent8_params {

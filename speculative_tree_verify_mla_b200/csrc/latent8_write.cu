@@ -72,6 +72,8 @@ __device__ inline int64_t find_slot(const WriteArgs& a, int i) {
   if (a.slot != nullptr) {
     slot = a.slot[i];
     if (slot == -1) return -1;
+    // a row that takes its position from the tree has to be one of its nodes
+    if (a.rot > 0 && a.pos.pos == nullptr && (i < a.tree_off[0] || i >= a.tree_off[a.batch])) return -3;
   } else {
     const int b = node_request(a.tree_off, a.batch, i);
     const int64_t at = b < 0 ? 0 : (int64_t)a.kv_off[b] + a.prefix_len[b] + (i - a.tree_off[b]);
