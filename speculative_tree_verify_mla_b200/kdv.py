@@ -442,16 +442,18 @@ _STRIDED = ("x", "y", "c", "k_rope", "q", "logits", "out", "hist", "allow")    #
 def _fill(p, kw: dict):
     """Fill a parameter struct: tensors become pointers (checked for device and
     element type, kept alive with the struct), HOST arrays are copied."""
-    p._keep, p._device = [], None
+    p._keep, p._device, p._host = [], None, []
     for k, v in kw.items():
         if k in ("h_prefix_len", "h_tree_T"):
             arr = (ctypes.c_int32 * len(v))(*[int(x) for x in v])
             p._keep.append(arr)
             setattr(p, k, ctypes.cast(arr, ctypes.POINTER(ctypes.c_int32)))
+            p._host.append((k, len(v), ctypes.addressof(arr)))
         elif k == "h_inv_freq" and v is not None:
             arr = np.array(v.numpy() if isinstance(v, torch.Tensor) else v, dtype=np.float64)
             p._keep.append(arr)
             p.h_inv_freq = arr.ctypes.data
+            p._host.append((k, arr.size, arr.ctypes.data))
         elif isinstance(v, torch.Tensor):
             if not v.is_cuda:
                 raise ValueError(f"{k}: a CUDA tensor is wanted")
@@ -469,8 +471,17 @@ def _fill(p, kw: dict):
     return p
 
 
+def _check_host(p) -> None:
+    """The HOST arrays that _fill copied have as many values as a call reads."""
+    for k, n, at in getattr(p, "_host", ()):
+        want = p.rot_dim // 2 if k == "h_inv_freq" else p.batch
+        if n < want and ctypes.cast(getattr(p, k), ctypes.c_void_p).value == at:   # (a caller may have set another array)
+            raise ValueError(f"{k}: {want} values are wanted, {n} given")
+
+
 def _launch(fn: str, p, stream) -> None:
     """Call an entry point on the device of the struct's tensors."""
+    _check_host(p)
     f = getattr(_lib or load(), fn)
     dev = getattr(p, "_device", None)
     if dev is None or dev == torch._C._cuda_getDevice():
@@ -518,6 +529,7 @@ def make_verify8_params(**kw) -> Verify8Params:
 
 
 def kdv_verify_attn8_workspace(params: Verify8Params) -> int:
+    _check_host(params)
     n = ctypes.c_size_t(0)
     _check(load().kdv_verify_attn8_workspace(ctypes.byref(params), ctypes.byref(n)), "kdv_verify_attn8_workspace")
     return int(n.value)
@@ -525,6 +537,7 @@ def kdv_verify_attn8_workspace(params: Verify8Params) -> int:
 
 def kdv_verify_attn8_plan(params: Verify8Params):
     """(splits per request, work items) that kdv_verify_attn8 would use."""
+    _check_host(params)
     splits = (ctypes.c_int32 * max(1, params.batch))()
     items = ctypes.c_int32(0)
     _check(load().kdv_verify_attn8_plan(ctypes.byref(params), splits, ctypes.byref(items)), "kdv_verify_attn8_plan")
