@@ -439,6 +439,11 @@ _FIELD_TYPES = {
 _STRIDED = ("x", "y", "c", "k_rope", "q", "logits", "out", "hist", "allow")    # their strides are fields of their own
 
 
+# the field that says what type a tensor of either type has
+_TYPE_CODES = {"x": "x_dtype", "y": "y_dtype", "c": "dtype", "k_rope": "dtype", "q": "dtype", "o": "out_dtype", "logits": "dtype",
+               "out": "out_dtype"}
+
+
 def _fill(p, kw: dict):
     """Fill a parameter struct: tensors become pointers (checked for device and
     element type, kept alive with the struct), HOST arrays are copied."""
@@ -461,6 +466,8 @@ def _fill(p, kw: dict):
                 raise ValueError(f"{k}: tensors of one call are on one device")
             if v.dtype not in _FIELD_TYPES[k]:
                 raise TypeError(f"{k}: unsupported dtype {v.dtype}")
+            if k in _TYPE_CODES and kw.get(_TYPE_CODES[k], KDV_BF16) != _FLOAT.index(v.dtype):
+                raise TypeError(f"{k}: {v.dtype} is not what {_TYPE_CODES[k]} says")
             if not (v.is_contiguous() or (k in _STRIDED and (v.dim() == 0 or v.stride(-1) == 1))):
                 raise ValueError(f"{k}: its elements have to be contiguous")
             p._device = v.device.index
