@@ -267,11 +267,12 @@ struct QueryRow {
   __device__ __forceinline__ static bool plain(uint32_t top) { return top == 0u || (top >= PLAIN_LATENT && top < 0x7f80u); }
   __device__ __forceinline__ static int plain_exponent(uint32_t top) { return top == 0u ? 0 : 7 + 127 - (int)(top >> 7); }
   // Any row: the same of its finite elements, but rope elements stay below 2^61. A row without latents goes by its rope part.
-  __device__ __forceinline__ int any_exponent() const {
+  __device__ __forceinline__ int any_exponent(bool& zeros) const {
     const uint32_t lat = finite_magnitude(), lo = rope & 0x7fffu, hi = (rope >> 16) & 0x7fffu;
     const uint32_t rp = __reduce_max_sync(0xffffffffu, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
     auto exponent = [](uint32_t m) { return m >= 0x80u ? (int)(m >> 7) - 127 : -102 - __clz(m); };   // floor(log2), m > 0
-    if (lat == 0u) return rp == 0u ? 0 : 7 - exponent(rp);
+    zeros = lat == 0u && rp == 0u;
+    if (lat == 0u) return zeros ? 0 : 7 - exponent(rp);
     return rp == 0u ? 7 - exponent(lat) : min(7 - exponent(lat), 60 - exponent(rp));
   }
   // Writes the row's terms times 2^e. bad: some element is not finite, or 2^e is no float.
@@ -558,14 +559,17 @@ __global__ void __launch_bounds__(THREADS, 1) verify8_tc_kernel(const __grid_con
       if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          e[k] = row[k].any_exponent();
+          bool zeros;
+          e[k] = row[k].any_exponent(zeros);
           row[k].stage<true>(e[k], 4 * warp + k, sp, lane);
+          if (zeros) e[k] = a.scale_exponent;        // logits of 0 take the factor 1 at any softmax scale
         }
       } else {                                       // four independent streams of instructions
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           e[k] = QueryRow::plain_exponent(top[k]);
           row[k].stage<false>(e[k], 4 * warp + k, sp, lane);
+          if (top[k] == 0u) e[k] = a.scale_exponent;
         }
       }
       if (lane < 4) {

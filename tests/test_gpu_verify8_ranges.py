@@ -126,6 +126,16 @@ def test_latent_and_rope_parts_of_different_magnitudes(lat, rope, rope_keys):
     compare(Run(c, TC, splits=1).go(), *f[:4])
 
 
+@pytest.mark.parametrize("others", [0, -124])
+def test_rows_of_zeros_at_any_softmax_scale(others):
+    """Queries of zeros weigh all keys alike, also beside rows of 2^-124 that a softmax scale of 2^120 brings back."""
+    c = one_token(66, 250)
+    c.q = (c.q.double() * (2.0 ** others if others else 0.0)).bfloat16()
+    c.q[::3] = 0.0
+    c.sm_scale = float(np.float32(c.sm_scale * 2.0 ** 124))
+    compare(Run(c, TC, splits=1).go(), *form(*of(c), c.sm_scale)[:4])
+
+
 def moves(ws):
     """How often a row's reference moves behind its first tile: ws log2 of the weights times scales, rows x keys."""
     n = np.zeros(len(ws), dtype=int)
