@@ -445,8 +445,9 @@ KDV_API kdv_status kdv_tree_build(const kdv_tree_build_params* p, void* stream);
  * KDV_ROPE_INTERLEAVED pairs elements (2k, 2k+1), KDV_ROPE_HALF (k, k +
  * rot_dim/2). Elements rot_dim..dim-1 are copied. inverse = 1 turns by -a:
  * the transpose, so it is the gradient of the forward turn (mscale included)
- * and moves already rotated rows back. Angles are formed in 64 bits, so
- * positions up to 2^31 keep an fp32 result's accuracy.
+ * and moves already rotated rows back. Angles are formed in 64 bits: for
+ * frequencies up to 1 their error is below half of fp32's step to positions of
+ * 2^27, and 5e-7 at 2^31.
  */
 #define KDV_ROPE_INTERLEAVED 0
 #define KDV_ROPE_HALF 1
@@ -626,8 +627,9 @@ KDV_API kdv_status kdv_verify_attn8(const kdv_verify8_params* p, void* stream);
  *   x = logits[t][v];  if seen: x > 0 ? x / repetition : x * repetition
  *   x = x - frequency * made - presence * [made > 0] + bias_b[v]
  *   out = -inf where the node's allow row has bit v clear, else x.
- * Arithmetic in fp32, rounded once to out_dtype. NaN logits stay NaN unless
- * their bit is clear.
+ * Arithmetic in fp32, rounded once to out_dtype; x / repetition is x times the
+ * fp32 value of 1 / repetition where that is a normal number. NaN logits stay NaN
+ * unless their bit is clear.
  */
 typedef struct kdv_logits_params {
   int32_t batch;           /* B in [1, KDV_MAX_BATCH]                            */

@@ -42,8 +42,9 @@ __device__ inline int32_t rope_position(const RopePos& r, int i) {
 }
 
 // (cos, sin) of pos * inv_freq, times mscale. The angle is formed in turns in
-// 64 bits and reduced to [-1/2, 1/2] there: a position of 2^31 leaves an
-// error below 2^31 * 2^-52 turns, far under fp32's own rounding of the result.
+// 64 bits and reduced to [-1/2, 1/2] there. The frequency in turns and the product round
+// by 2^-53 each: for frequencies up to 1, 5e-7 radians at a position of 2^31, and below half
+// of fp32's step of the result to 2^27.
 __device__ inline float2 rope_cos_sin(int32_t pos, double turns_per_pos, float mscale) {
   double t = (double)pos * turns_per_pos;
   t -= rint(t);

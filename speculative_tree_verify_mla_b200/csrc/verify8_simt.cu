@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) combine8_kernel(const __grid_co
 
 // The same for the tensor-core kernel's parts (fp16, 512 dims): one warp half a row, no barrier;
 // the first eight parts are on their way before their weights are known. 5.5k layer (832 rows, 10
-// parts): 28.4 us in all, 28.7 with a warp a row and four parts in flight; and 0.4 us more with a CTA a row as above.
+// parts): 0.3 us more with a warp a row and four parts in flight, 0.7 with a CTA a row as above (28.4 us in all then, 26.2 now).
 constexpr int ROW_WARPS = 4;
 __global__ void __launch_bounds__(ROW_WARPS * 32) combine8_rows_kernel(const __grid_constant__ Verify8Args a,
                                                                        const __grid_constant__ VerifyPlan p) {

@@ -47,11 +47,13 @@
 //               the reference by 2^7 (a vote), then O is rescaled in TMEM.
 //
 // What bounds it: the tensor core and shared memory. A tile's 16 (N = 128) + 4 + 36 (N = 64) MMAs take
-// 2.55k clocks alone and 3.3k beside the copies and the softmax; one cp.async block of 12 KB takes
-// ~400. Over 200k keys the part runs into its power cap: 470 us in bursts, 550 us sustained (16
-// nodes x 64 heads, 948 and 810 TFLOP/s of the logical products). Contiguous pools through TMA
+// 2.55k clocks alone and 3.4k beside the copies and the softmax (71 % of them tensor-active over 200k keys); one
+// cp.async block of 12 KB takes ~400. Over 200k keys the part runs into its power cap: 461 us in bursts (about 1.7 GHz),
+// 529 us sustained (1.58 GHz; 16 nodes x 64 heads, 967 and 843 TFLOP/s of the logical products, 2176 a row and key).
+// As bf16 products its own operations are 2688 of them, 323 us at the measured 1702 TFLOP/s. Contiguous pools through TMA
 // boxes instead of the gather: 20 and 11 us more, so there is one way to bring keys in. Few rows over short contexts: 16k
-// clocks an item for set-up, queries, first tile and output, and the merge (2.5-4 us): 13 nodes x 64 heads x 5.5k keys 26.5 us.
+// clocks an item for set-up, queries, first tile and output, and the merge (2.5-4 us): 13 nodes x 64 heads x 5.5k keys 26.2 us.
+// (Device times in a graph with the cache warm, but for the 200k keys. 96 registers a thread, 12 bytes of them spilled.)
 #include <cuda_fp8.h>
 
 #include "sm100_ptx.cuh"
